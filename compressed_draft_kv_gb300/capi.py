@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(HERE, "libmasw.so")
 
 MASW_OK, MASW_EINVAL, MASW_ENOMEM, MASW_ECAPACITY, MASW_ESTATE, MASW_ECUDA, MASW_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6
 MASW_EGUARD = -7
-MASW_F32, MASW_BF16 = 0, 1
+MASW_F32, MASW_BF16, MASW_E4M3 = 0, 1, 2
 MASW_MAX_BATCH, MASW_MAX_GROUP = 512, 8
 
 # every symbol include/masw.h declares
@@ -26,7 +26,7 @@ EXPORTS = [
     "masw_verify_attn", "masw_verify_workspace_bytes", "masw_verify_attn_noalloc", "masw_mem_load", "masw_mem_export",
     "masw_query", "masw_sync", "masw_index", "masw_version", "masw_check_guards",
     "masw_greedy_accept", "masw_greedy_workspace_bytes", "masw_eq1_speedup", "masw_prefill",
-    "masw_selftest_timeout",
+    "masw_selftest_timeout", "masw_paged_append", "masw_paged_attn", "masw_paged_workspace_bytes",
 ]
 
 
@@ -47,6 +47,17 @@ class masw_state_t(ctypes.Structure):
                                             "ring_rows", "rows", "slot_capacity")]
 
 
+class masw_paged_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("page_stride", ctypes.c_longlong)] + \
+               [(n, ctypes.c_int) for n in ("dtype", "n_pages", "page_size", "n_kv_heads", "head_dim", "batch",
+                                            "table_stride")]
+
+
+class masw_rope_t(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p)] + [(n, ctypes.c_int) for n in ("n_pos", "rot_dim", "interleaved")]
+
+
 _lib = None
 
 
@@ -59,6 +70,7 @@ def load() -> ctypes.CDLL:
         raise ImportError(f"libmasw.so not built at {LIB_PATH}; run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    L = ctypes.c_longlong
     IP = ctypes.POINTER(ctypes.c_int)
     sig = {
         "masw_mem_create": [I, I, I, I, I, I, ctypes.POINTER(masw_opts_t), ctypes.POINTER(P)],
@@ -84,6 +96,9 @@ def load() -> ctypes.CDLL:
         "masw_index": [I, I, I, I, I, I],
         "masw_greedy_accept": [P, P, I, I, I, I, P, P, P, Z, P],
         "masw_greedy_workspace_bytes": [I, I, I, ctypes.POINTER(Z)],
+        "masw_paged_append": [P, P, P, I, P, P, L, L, P, P, P, P, I, L, P, P],
+        "masw_paged_attn": [P, P, P, I, I, P, I, L, I, F, P, I, P, P, P, Z, P],
+        "masw_paged_workspace_bytes": [P, I, I, I, ctypes.POINTER(Z)],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -269,6 +284,128 @@ def masw_greedy_workspace_bytes(B, L, V) -> int:
 
 def masw_eq1_speedup(l_acc, l_draft, t_draft, t_target) -> float:
     return load().masw_eq1_speedup(l_acc, l_draft, t_draft, t_target)
+
+
+# ------------------------------------------------------------ paged caches --
+
+def masw_paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> masw_paged_t:
+    """Describe a paged cache to the calls below: k, v [n_pages, Hkv, page_size, D] (bf16, or float8_e4m3fn / uint8
+    bytes of e4m3 with fp32 scales [n_pages, Hkv]), page_table [batch, stride] int32.  Pages may lie apart (a view of
+    a larger array), their inside is dense.  The description holds the tensors; make it once per cache."""
+    import torch
+    e4 = k.dtype in (torch.float8_e4m3fn, torch.uint8)
+    if not e4 and k.dtype != torch.bfloat16:
+        raise ValueError("pages must be bfloat16 or float8_e4m3fn")
+    n, h, p, d = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype or (n > 1 and v.stride(0) != k.stride(0)):
+        raise ValueError("k and v pages must have the same shape, type and page stride")
+    for x in (k, v):
+        if tuple(x.stride()[1:]) != (p * d, d, 1):
+            raise ValueError("a page must be dense")
+    if e4:
+        for x in (k_scale, v_scale):
+            if x is None or x.dtype != torch.float32 or tuple(x.shape) != (n, h) or not x.is_contiguous():
+                raise ValueError("e4m3 pages need contiguous fp32 scales [n_pages, Hkv] for k and v")
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("bf16 pages have no scales")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be int32 [batch, stride] with dense rows")
+    tensors = [x for x in (k, v, page_table, k_scale, v_scale) if x is not None]
+    if len({x.device for x in tensors}) != 1:
+        raise ValueError("the cache's tensors must lie on one device")
+    B = page_table.shape[0]
+    c = masw_paged_t(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), k.stride(0) if n > 1 else 0,
+                     MASW_E4M3 if e4 else MASW_BF16, n, p, h, d, B,
+                     page_table.stride(0) if B > 1 else page_table.shape[1])
+    c.tensors = tensors
+    c.device, c.bf16, c.int32, c.f32 = k.device, torch.bfloat16, torch.int32, torch.float32
+    return c
+
+
+def masw_rope(cos_sin, interleaved=False) -> masw_rope_t:
+    """Rotary table for masw_paged_append: cos_sin [n_pos, rot_dim] fp32, each row the cosines, then the sines."""
+    import torch
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous fp32 [n_pos, rot_dim]")
+    r = masw_rope_t(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved))
+    r.tensors = [cos_sin]
+    return r
+
+
+def _token_rows(name, x, heads, dim, cache):
+    """Token stride of x [rows, heads, dim] (bf16 on the cache's device; heads and elements dense)."""
+    if x.dtype != cache.bf16 or x.device != cache.device or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{name} must be bfloat16 [rows, {heads}, {dim}] on the cache's device")
+    st = x.stride()
+    if st[2] != 1 or (st[1] != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return st[0] if x.shape[0] > 1 else 0
+
+
+def _ints(name, x, n, cache):
+    if x is not None and (x.dtype != cache.int32 or x.device != cache.device or x.numel() < n or not x.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous int32 with at least {n} elements on the cache's device")
+    return _ptr(x)
+
+
+def masw_paged_append(cache, kv_len, k, v, rope=None, pos=None, q=None, q_out=None, row_start=None, status=None,
+                      stream=None):
+    """Append the K/V rows [rows, Hkv, D] of new tokens to a paged cache, K (and q -> q_out [rows, Hq, D]) rotated by
+    `rope` on the way.  kv_len [batch] counts them already; row_start [batch + 1] says whose rows are whose (None:
+    rows / batch each).  k, v and q may be slices of a fused projection.  status: optional int32 word."""
+    rows, (B, H, D) = k.shape[0], (cache.batch, cache.n_kv_heads, cache.head_dim)
+    ks, vs = _token_rows("k", k, H, D, cache), _token_rows("v", v, H, D, cache)
+    hq = qs = 0
+    if q is not None:
+        hq = q.shape[1]
+        qs = _token_rows("q", q, hq, D, cache)
+        if q_out is None or q_out.dtype != q.dtype or q_out.shape != q.shape or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous bfloat16 of q's shape")
+    if v.shape[0] != rows or (q is not None and q.shape[0] != rows):
+        raise ValueError("k, v and q differ in rows")
+    _check(load().masw_paged_append(ctypes.byref(cache), _ints("kv_len", kv_len, B, cache),
+                                    _ints("row_start", row_start, B + 1, cache), rows, _ptr(k), _ptr(v), ks, vs,
+                                    None if rope is None else ctypes.byref(rope), _ints("pos", pos, rows, cache),
+                                    _ptr(q), _ptr(q_out), hq, qs, _ints("status", status, 1, cache),
+                                    _device_stream(stream, cache)))
+
+
+def masw_paged_workspace_bytes(cache, rows, max_rows, n_q_heads) -> int:
+    out = ctypes.c_size_t()
+    _check(load().masw_paged_workspace_bytes(ctypes.byref(cache), rows, max_rows, n_q_heads, ctypes.byref(out)))
+    return out.value
+
+
+def masw_paged_attn(cache, kv_len, q, o, lse=None, row_start=None, max_rows=None, window=0, scale=0.0, status=None,
+                    workspace=None, stream=None):
+    """Causal attention of q [rows, Hq, D] bf16 over a paged cache -> o [rows, Hq, D] (bf16 or fp32), lse [rows, Hq]
+    fp32.  With row_start, max_rows bounds the rows of one sequence (None: all of them).  Without a workspace (uint8,
+    masw_paged_workspace_bytes), one is allocated."""
+    rows, hq, D = q.shape
+    B = cache.batch
+    qs = _token_rows("q", q, hq, cache.head_dim, cache)
+    if o.shape != q.shape or not o.is_contiguous() or o.device != cache.device or o.dtype not in (cache.bf16, cache.f32):
+        raise ValueError("o must be contiguous bfloat16 or float32 of q's shape")
+    if lse is not None and (tuple(lse.shape) != (rows, hq) or lse.dtype != cache.f32 or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [rows, Hq]")
+    mr = rows if max_rows is None else max_rows
+    if row_start is None:
+        mr = rows // B
+    if workspace is None:
+        import torch
+        workspace = torch.empty(masw_paged_workspace_bytes(cache, rows, mr, hq), dtype=torch.uint8, device=cache.device)
+    _check(load().masw_paged_attn(ctypes.byref(cache), _ints("kv_len", kv_len, B, cache),
+                                  _ints("row_start", row_start, B + 1, cache), rows, mr, _ptr(q), hq, qs, window, scale,
+                                  _ptr(o), MASW_BF16 if o.dtype == cache.bf16 else MASW_F32, _ptr(lse),
+                                  _ints("status", status, 1, cache), _ptr(workspace), workspace.numel(),
+                                  _device_stream(stream, cache)))
+
+
+def _device_stream(stream, cache):
+    import torch
+    if torch.cuda.is_available() and cache.device.type == "cuda" and cache.device.index != torch.cuda.current_device():
+        raise ValueError("the cache lies on another device than the current one")
+    return _stream(stream)
 
 
 # ---------------------------------------------------------------- plumbing --

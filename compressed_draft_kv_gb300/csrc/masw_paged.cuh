@@ -1,0 +1,88 @@
+// What the paged-cache operators share: checked arguments, the parameters that
+// describe a cache to a kernel, and the e4m3 conversions.
+#pragma once
+
+#include "masw_internal.cuh"
+
+namespace masw {
+
+// a paged cache as its kernels see it (strides in bytes)
+struct PagedView {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;          // null: bf16 pages
+    float* v_scale;
+    const int* table;        // [batch][table_stride]
+    long long page_bytes;    // between consecutive pages
+    int n_pages, P, Hkv, D, B, table_stride;
+    int cap;                 // tokens a table row can hold
+};
+
+// The rows of sequence b: [r0, r0 + n), at positions kv - n ..  `ok` is false
+// (and n = 0) when the row range or the length cannot be what the caller meant.
+struct SeqRows {
+    int r0, n, kv;
+    bool ok;
+};
+__host__ __device__ inline SeqRows seq_rows_of(int r0, int r1, int kv, int rows, int cap) {
+    SeqRows s{r0, r1 - r0, kv, true};
+    s.ok = r0 >= 0 && r1 >= r0 && r1 <= rows && kv >= 0 && kv <= cap;
+    if (!s.ok) s.n = s.kv = 0;
+    return s;
+}
+__device__ __forceinline__ SeqRows seq_rows(const int* row_start, const int* kv_len, int b, int rows, int B, int cap) {
+    const int per = rows / B;
+    const int r0 = row_start ? row_start[b] : b * per, r1 = row_start ? row_start[b + 1] : r0 + per;
+    return seq_rows_of(r0, r1, kv_len[b], rows, cap);
+}
+
+// Units of an append: (sequence, touched page) pairs in a one-dimensional grid
+// that the host can size without knowing the lengths.  n rows touch at most
+// n / P + 2 pages, so sequence b owns units [r0 / P + 2 b, next): the next
+// sequence's first unit lies at least n / P + 2 behind.
+__host__ __device__ inline int append_unit_base(int r0, int b, int P) { return r0 / P + 2 * b; }
+__host__ __device__ inline int append_units(int rows, int B, int P) { return rows / P + 2 * B; }
+
+// smallest power of two s with amax <= 448 s, clamped to [2^-64, 2^119]; 1 for 0
+__host__ __device__ inline int pow2_scale_exp(uint32_t amax_bits) {
+    const int ex = (int)(amax_bits >> 23) - 127;
+    const int e = (amax_bits & 0x7fffffu) <= 0x600000u ? ex - 8 : ex - 7;   // 448 = 1.75 * 2^8
+    return amax_bits == 0u ? 0 : (e < -64 ? -64 : (e > 119 ? 119 : e));
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float pow2_scale(float amax) {
+    return __uint_as_float((uint32_t)(pow2_scale_exp(__float_as_uint(amax)) + 127) << 23);
+}
+// |x|, or 0 for infinities and NaN
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= 3.4028234663852886e38f ? a : 0.f;
+}
+// two fp32 values -> e4m3 (round to nearest even, lo in bits 0..7); what is not
+// finite becomes NaN (the conversion itself would saturate an infinity)
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    lo = fabsf(lo) <= 3.4028234663852886e38f ? lo : __int_as_float(0x7fffffff);
+    hi = fabsf(hi) <= 3.4028234663852886e38f ? hi : __int_as_float(0x7fffffff);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// two e4m3 values (bits 0..7 and 8..15) -> f16x2
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)v));
+    return r;
+}
+__device__ __forceinline__ void f16x2_to_f32(uint32_t v, float& lo, float& hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v));
+}
+#endif
+
+}  // namespace masw
+
+// Argument checks shared by the paged calls; fills `view`.  0 or a status with
+// the message set.
+int masw_paged_view(const masw_paged_t* cache, const char* who, masw::PagedView* view);

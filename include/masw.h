@@ -66,6 +66,7 @@ extern "C" {
 /* ---- element types ------------------------------------------------------- */
 #define MASW_F32   0
 #define MASW_BF16  1
+#define MASW_E4M3  2   /* 8-bit float (4 exponent, 3 mantissa bits, no infinity): paged caches only */
 
 /* ---- limits --------------------------------------------------------------- */
 #define MASW_MAX_BATCH  512   /* sequences per handle */
@@ -305,6 +306,120 @@ int masw_verify_attn_noalloc(const void* q, const void* k_cache, const void* v_c
                              const int* kv_len, int B, int Lq, int Hq, int Hkv, int D,
                              int Tmax, int dtype, float scale, float* o, float* lse,
                              int* status, masw_stream_t stream);
+
+/* ---- paged caches ------------------------------------------------------------- */
+
+/* A K/V cache in pages of page_size tokens, owned by the caller: what a server
+ * keeps for the target model, whose verify step ([EN] §3.3 Algorithm 2) appends
+ * the drafted tokens' keys and values and attends over the whole prefix.  Token
+ * position p of sequence b is row p % page_size of page
+ * page_table[b * table_stride + p / page_size].
+ *   k, v: device [n_pages][n_kv_heads][page_size][head_dim], elements of `dtype`
+ *     (MASW_BF16 or MASW_E4M3), 16-byte aligned; consecutive pages lie
+ *     page_stride elements apart (0: n_kv_heads * page_size * head_dim; else at
+ *     least that, and a multiple of 16 bytes), so K and V pages may be
+ *     interleaved in one array.
+ *   k_scale, v_scale: device float [n_pages][n_kv_heads] (MASW_E4M3; NULL for
+ *     bf16): an element stands for its e4m3 value times the scale of its page
+ *     and head.  masw_paged_append writes powers of two in [2^-64, 2^119];
+ *     masw_paged_attn takes any positive finite scale in that range.
+ *   page_table: device int [batch][table_stride].  Entries of pages at or behind
+ *     a sequence's end are not read.  Sequences may share pages that none of them
+ *     appends to.
+ * head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; batch <= MASW_MAX_BATCH;
+ * table_stride * page_size below 2^31.  Page ids outside [0, n_pages) and lengths
+ * that the table cannot hold are found on the device, never followed, and
+ * recorded in the call's status word. */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int* page_table;
+    long long page_stride;
+    int dtype;
+    int n_pages;
+    int page_size;
+    int n_kv_heads;
+    int head_dim;
+    int batch;
+    int table_stride;
+} masw_paged_t;
+
+/* Rotary positions: cos_sin is a device float table [n_pos][rot_dim], row p the
+ * rot_dim / 2 cosines of position p's angles, then their sines (16-byte aligned).
+ * The first rot_dim elements of each head are rotated (rot_dim a multiple of 16,
+ * at most head_dim), the others kept.  Pair i is (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) with interleaved = 1; (a, b) becomes (a c - b s, b c + a s),
+ * computed in fp32 with each product and sum rounded once. */
+typedef struct {
+    const float* cos_sin;
+    int n_pos;
+    int rot_dim;
+    int interleaved;
+} masw_rope_t;
+
+/* Append the K/V rows of new tokens to a paged cache, rotating K (and Q) on the
+ * way, in one launch.  `rows` new tokens in all: those of sequence b are rows
+ * row_start[b] .. row_start[b + 1] - 1 (device int [batch + 1], non-decreasing;
+ * NULL: rows / batch each) and go to positions kv_len[b] - n_b .. kv_len[b] - 1:
+ * kv_len (device int [batch]) counts them already.  Rows outside
+ * [row_start[0], row_start[batch]) are padding: not read, and their q_out rows
+ * left as they were.  A sequence without rows is left alone.
+ * k, v: device bf16 [rows][n_kv_heads][head_dim], token rows k_stride / v_stride
+ * elements apart (0: dense; a multiple of 8), e.g. slices of a fused projection.
+ * rope: NULL stores K as it is (and copies Q).  pos: device int [rows], the rotary
+ * position of each row, or NULL: its cache position.  Positions outside
+ * [0, n_pos) set the status and leave their row unrotated.
+ * q: NULL, or device bf16 [rows][n_q_heads][head_dim] with token stride q_stride;
+ * its rotated rows go to q_out (bf16, dense; q_out == q is allowed when q is
+ * dense).
+ * bf16 pages: the fp32 rotation is rounded once.  e4m3 pages, for each touched
+ * page, kv head and K or V: with A the largest finite magnitude of the new rows
+ * there, the scale becomes s = the smallest power of two with A <= 448 s (1 if
+ * A = 0) where the call writes the page's row 0, and max(old scale, s) otherwise
+ * (the old one if A = 0); when it grows, the rows before the new ones are rounded
+ * again to the new scale.  An element is stored as its fp32 value over the scale,
+ * rounded to nearest even; infinities and NaN are stored as NaN.  The result does
+ * not depend on timing.  A scale never shrinks while its page is being filled:
+ * after drafts were rejected (a shorter kv_len), the next append overwrites their
+ * rows and keeps the scale.
+ * No page may be appended to for two sequences in one call.  status: device int
+ * or NULL; the call writes MASW_EINVAL there when it met a bad length, row range,
+ * page id or position (and skips what it cannot place), and nothing otherwise. */
+int masw_paged_append(const masw_paged_t* cache, const int* kv_len, const int* row_start, int rows,
+                      const void* k, const void* v, long long k_stride, long long v_stride,
+                      const masw_rope_t* rope, const int* pos, const void* q, void* q_out, int n_q_heads,
+                      long long q_stride, int* status, masw_stream_t stream);
+
+/* Causal attention of the `rows` query rows over a paged cache ([EN] §2.3 Eq. 2,
+ * §3.3 Algorithm 2).  Rows belong to sequences as in masw_paged_append (one row
+ * each: decode; L_draft + 1: verify; many: a chunk of a prompt); query j of the
+ * n_b rows of sequence b stands at position p = kv_len[b] - n_b + j and sees keys
+ * 0..p, or with window > 0 only p - window + 1 .. p.  A row that sees no key gets
+ * O = 0 and LSE = -inf.
+ * q: device bf16 [rows][n_q_heads][head_dim], token stride q_stride elements (0:
+ * dense; a multiple of 8); n_q_heads a multiple of n_kv_heads, at most 128 query
+ * heads per kv head.  max_rows: at least every n_b (NULL row_start: ignored).
+ * o: device [rows][n_q_heads][head_dim], bf16 or float (o_dtype), dense, 16-byte
+ * aligned; lse: device float [rows][n_q_heads] or NULL.  scale 0 ->
+ * 1/sqrt(head_dim).  Keys behind a sequence's end may hold anything, NaN included.
+ * A non-finite value at a key that a sequence's queries partly see may reach those
+ * of its rows that share a tile with a row that sees it.
+ * Scores, softmax statistics and sums are fp32 (e4m3 pages: Q enters as two e4m3
+ * terms, at least 14 bits below the largest element of its rows).
+ * workspace: device scratch of masw_paged_workspace_bytes() bytes, 16-byte
+ * aligned; needs no initialisation and must not be shared by calls that overlap on
+ * the GPU.  status: device int or NULL; the call writes there MASW_EINVAL for a
+ * bad length, row range or page id, MASW_ETIMEOUT when a bounded wait gave up
+ * (the outputs concerned are then undefined), and nothing otherwise. */
+int masw_paged_attn(const masw_paged_t* cache, const int* kv_len, const int* row_start, int rows, int max_rows,
+                    const void* q, int n_q_heads, long long q_stride, int window, float scale,
+                    void* o, int o_dtype, float* lse, int* status, void* workspace, size_t workspace_bytes,
+                    masw_stream_t stream);
+
+/* Bytes of workspace masw_paged_attn needs for these sizes on the current device. */
+int masw_paged_workspace_bytes(const masw_paged_t* cache, int rows, int max_rows, int n_q_heads, size_t* bytes);
 
 /* ---- speculative acceptance ------------------------------------------------------ */
 
