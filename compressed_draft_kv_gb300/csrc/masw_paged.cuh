@@ -50,6 +50,30 @@ __host__ __device__ inline int pow2_scale_exp(uint32_t amax_bits) {
     return amax_bits == 0u ? 0 : (e < -64 ? -64 : (e > 119 ? 119 : e));
 }
 
+// ---- how attention over few query rows is cut over CTAs --------------------
+// The keys of one (sequence, kv head) pair come in tiles of 128.  All pairs'
+// tiles form one line, sequence by sequence and head by head, and CTA c of C
+// takes tiles [first_tile(c), first_tile(c + 1)) of it: every CTA gets the same
+// number of tiles (give or take one) whatever the lengths are.  A pair that is
+// cut leaves one partial result for each CTA that holds a piece of it: in that
+// CTA's slot 0 if the piece is the CTA's first, else in its slot 1 (its last).
+constexpr int kTile = 128;
+struct TileRange {
+    int lo, hi;   // visible keys of the sequence's rows: [lo, hi)
+    int t0, nt;   // first tile and number of tiles (at least one: it writes the outputs)
+};
+__host__ __device__ inline TileRange tile_range(int n, int kv, int window) {
+    TileRange r{0, kv, 0, 0};
+    if (n < 1) return r;
+    if (window > 0 && kv - n - window + 1 > 0) r.lo = kv - n - window + 1;
+    r.t0 = r.lo / kTile;
+    r.nt = (r.hi + kTile - 1) / kTile - r.t0;
+    if (r.nt < 1) r.nt = 1;
+    return r;
+}
+__host__ __device__ inline int first_tile(int c, int total, int C) { return (int)((long long)c * total / C); }
+__host__ __device__ inline int tile_owner(int t, int total, int C) { return (int)((((long long)t + 1) * C - 1) / total); }
+
 #ifdef __CUDACC__
 __device__ __forceinline__ float pow2_scale(float amax) {
     return __uint_as_float((uint32_t)(pow2_scale_exp(__float_as_uint(amax)) + 127) << 23);

@@ -5,25 +5,12 @@
 // query head of the group).  Keys pass through shared memory in fp32, 32 at a
 // time; a warp owns two rows, its lanes hold a score each and four output
 // elements each, with the running maximum and sum of the softmax.
-#include "masw_paged.cuh"
+#include "masw_paged_attn.cuh"
 
 #include <algorithm>
 #include <cstring>
 
 namespace masw {
-
-struct PagedAttnParams {
-    PagedView c;
-    const int* kv_len;
-    const int* row_start;
-    const __nv_bfloat16* q;   // [rows][Hq][D], token stride q_stride
-    long long q_stride;
-    void* o;
-    float* lse;
-    int* status;
-    int rows, max_rows, Hq, G, window, o_f32;
-    float scale;
-};
 
 constexpr int kSimpleRows = 16, kSimpleKeys = 32;
 
@@ -137,7 +124,38 @@ static int paged_attn_sizes(const PagedView& c, const char* who, int rows, int m
     if (n_q_heads < c.Hkv || n_q_heads % c.Hkv || n_q_heads / c.Hkv > 128)
         return fail("n_q_heads must be a multiple of n_kv_heads, at most 128 per kv head");
     *mr = ragged ? std::min(max_rows, rows) : rows / c.B;
+    if ((long long)c.B * c.Hkv * (c.cap / kTile + 2) > 0x7fffffffll) return fail("batch * heads * table too large");
     return MASW_OK;
+}
+
+static int device_sms(int* sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return masw_set_error(nullptr, MASW_ECUDA, "paged_attn: cannot query the current device");
+    }
+    return MASW_OK;
+}
+
+static size_t workspace_bytes_for(const PagedView& c, int max_rows, int G, int sms) {
+    if ((long long)max_rows * G > kRowsMax) return 16;
+    return (size_t)sms * 2 * kRowsMax * (c.D + 2) * sizeof(float);   // two partials a CTA
+}
+
+// pages as a 4-d tensor [n_pages][Hkv][P][D], boxes of one page's rows (at most
+// 128) and one 128-byte (or narrower) column panel, swizzled as the matrix
+// descriptors say
+static bool make_page_map(CUtensorMap* map, const PagedView& c, const uint8_t* base) {
+    const int esize = c.k_scale ? 1 : 2, row = c.D * esize, panel = std::min(row, 128);
+    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.P, (cuuint64_t)c.Hkv, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)row, (cuuint64_t)c.P * row, (cuuint64_t)c.page_bytes};
+    const cuuint32_t box[4] = {(cuuint32_t)(panel / esize), (cuuint32_t)std::min(c.P, kTile), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return tma_encode_fn()(map, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                           const_cast<uint8_t*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           panel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 extern "C" int masw_paged_workspace_bytes(const masw_paged_t* cache, int rows, int max_rows, int n_q_heads, size_t* bytes) {
@@ -147,7 +165,9 @@ extern "C" int masw_paged_workspace_bytes(const masw_paged_t* cache, int rows, i
     int mr = 0;
     if (!rc) rc = paged_attn_sizes(c, "paged_workspace", rows, max_rows, true, n_q_heads, &mr);
     if (rc) return rc;
-    *bytes = 16;
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    *bytes = workspace_bytes_for(c, mr, n_q_heads / c.Hkv, sms);
     return MASW_OK;
 }
 
@@ -172,10 +192,14 @@ extern "C" int masw_paged_attn(const masw_paged_t* cache, const int* kv_len, con
     if (((uintptr_t)q | (uintptr_t)o | (uintptr_t)workspace) & 15) return fail("q, o and workspace must be 16-byte aligned");
     if (((uintptr_t)kv_len | (uintptr_t)row_start | (uintptr_t)lse | (uintptr_t)status) & 3)
         return fail("kv_len, row_start, lse and status must be 4-byte aligned");
-    size_t need = 0;
-    if ((rc = masw_paged_workspace_bytes(cache, rows, mr, n_q_heads, &need))) return rc;
-    if (workspace_bytes < need) return fail("workspace too small");
+    int sms = 0;
+    if ((rc = device_sms(&sms))) return rc;
+    if (workspace_bytes < workspace_bytes_for(p.c, mr, n_q_heads / p.c.Hkv, sms)) return fail("workspace too small");
     if (rows == 0 || mr == 0) return MASW_OK;
+    if (!tma_encode_fn()) return masw_set_error(nullptr, MASW_ECUDA, "paged_attn: cuTensorMapEncodeTiled is unavailable");
+    if (!make_page_map(&p.tm_k, p.c, p.c.k) || !make_page_map(&p.tm_v, p.c, p.c.v))
+        return fail("cannot describe the pages as TMA tensors");
+    p.part = (float*)workspace;
     p.kv_len = kv_len;
     p.row_start = row_start;
     p.q = (const __nv_bfloat16*)q;
@@ -189,6 +213,12 @@ extern "C" int masw_paged_attn(const masw_paged_t* cache, const int* kv_len, con
     p.window = window;
     p.o_f32 = o_dtype == MASW_F32;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)p.c.D);
+    p.scale_log2 = p.scale * 1.4426950408889634f;
+    if (mr * p.G <= kRowsMax) {
+        const cudaError_t e = launch_paged_rows(p, sms, (cudaStream_t)stream);
+        if (e != cudaSuccess) return masw_set_error(nullptr, MASW_ECUDA, std::string("paged_attn: ") + cudaGetErrorString(e));
+        return MASW_OK;
+    }
     const size_t smem = (size_t)(kSimpleRows * p.c.D + 2 * kSimpleKeys * (p.c.D + 1)) * sizeof(float);
     const long long tiles = ((long long)mr * p.G + kSimpleRows - 1) / kSimpleRows;
     const cudaError_t e = masw_launch(paged_attn_kernel, dim3((unsigned)tiles, p.c.Hkv, p.c.B), dim3(256), smem,
