@@ -54,7 +54,8 @@ __host__ __device__ inline int pow2_scale_exp(uint32_t amax_bits) {
 // The keys of one (sequence, kv head) pair come in tiles of 128.  All pairs'
 // tiles form one line, sequence by sequence and head by head, and CTA c of C
 // takes tiles [first_tile(c), first_tile(c + 1)) of it: every CTA gets the same
-// number of tiles (give or take one) whatever the lengths are.  A pair that is
+// number of tiles (give or take one; CTAs behind the last tile get none) whatever
+// the lengths are.  A pair that is
 // cut leaves one partial result for each CTA that holds a piece of it: in that
 // CTA's slot 0 if the piece is the CTA's first, else in its slot 1 (its last).
 constexpr int kTile = 128;
@@ -71,8 +72,15 @@ __host__ __device__ inline TileRange tile_range(int n, int kv, int window) {
     if (r.nt < 1) r.nt = 1;
     return r;
 }
-__host__ __device__ inline int first_tile(int c, int total, int C) { return (int)((long long)c * total / C); }
-__host__ __device__ inline int tile_owner(int t, int total, int C) { return (int)((((long long)t + 1) * C - 1) / total); }
+// tiles of every CTA: total / C, one more for the first total % C
+__host__ __device__ inline int first_tile(int c, int total, int C) {
+    const int q = total / C, rem = total - q * C;
+    return c * q + (c < rem ? c : rem);
+}
+__host__ __device__ inline int tile_owner(int t, int total, int C) {
+    const int q = total / C, rem = total - q * C;
+    return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q;
+}
 
 #ifdef __CUDACC__
 __device__ __forceinline__ float pow2_scale(float amax) {

@@ -37,7 +37,7 @@ __device__ __forceinline__ void store_out(const PagedAttnParams& p, size_t at, f
 // threads.  A sequence whose rows or length are not possible has no tiles.
 template <int NT>
 __device__ int make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n, int* s_r0, bool report) {
-    constexpr int kPer = MASW_MAX_BATCH / NT;
+    constexpr int kPer = (MASW_MAX_BATCH + NT - 1) / NT;
     __shared__ int warp_sum[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, B = p.c.B;
     int mine[kPer], sum = 0;

@@ -16,18 +16,22 @@
 //   * O^T += V^T P^T with head_dim as M: V is read as it lies in the page;
 //   * e4m3 pages enter the tensor cores as they are.  Q is split into two e4m3
 //     terms (q1 + q2 / 16, exact for bf16 unless an element is 2^-21 of the
-//     largest) and the weights into three (p1 + p2 / 16 + p3 / 256 of their fp16
-//     value, 2^-12 relative): the terms lie side by side in N, so a tile of K or
-//     V is read by the tensor core once for all of them.  The scale of a key's
+//     largest), and so are the weights (p1 + p2 / 16, off by at most 2^-9, half of
+//     what rounding them to bf16 would cost): the terms lie side by side in N, so a
+//     tile of K or V is read by the tensor core once for both.  The scale of a key's
 //     page multiplies its scores; the scale of its value's page enters the
 //     exponent, 2^(s + log2 scale - reference), and the sum takes it out again;
 //   * bf16 pages: weights as two bf16 terms (2^-17).
 // Rows behind the end of a sequence never count: their scores are masked, and
 // their V rows are zeroed in shared memory (0 x NaN is NaN in a matrix product).
 //
-// Warps 0-3: softmax and outputs; 4: issues S; 5: issues O; 6: page ids, scales
-// and TMA; 7: loads and splits Q for the next pair.  Hand-offs are mbarriers;
-// every wait is bounded.
+// Warps 0-3 and 4-7: two softmax groups that take the tiles in turn, each with its
+// own S, P, O, sums and reference (a tile's chain of barriers, votes and TMEM
+// loads is ~1000 cycles long whatever the work in it; one group alone left half of
+// the stream's bandwidth unused); the first group joins the two at a pair's end.
+// Warp 8 issues S, 9 issues O, 10 looks up pages and scales and issues TMA, 11
+// loads and splits Q for the next pair.  Hand-offs are mbarriers; every wait is
+// bounded.
 #include "masw_paged_attn.cuh"
 
 namespace masw {
@@ -35,7 +39,7 @@ namespace rows {
 
 using namespace tc;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kMeta = 16;    // tiles of scales kept: more than a stage ring's tiles in flight
 
 template <bool E4, int D, int NP>
@@ -48,41 +52,74 @@ struct Cfg {
     static constexpr uint32_t kTileB = kTile * kRB;
     static constexpr uint32_t kSwz = kPB == 128 ? 2 : 4;        // 128- or 64-byte swizzle
     static constexpr uint32_t kAtom = 8 * kPB;                  // 8 rows
-    static constexpr int kSN = E4 ? 2 * NP : (NP < 16 ? 16 : NP);            // columns of S^T
-    static constexpr int kPN = E4 ? (NP == 8 ? 32 : 3 * NP) : 2 * NP;        // columns of P^T and O^T
-    static constexpr int kTerms = E4 ? 3 : 2;
+    static constexpr int kSN = E4 ? 2 * NP : (NP + 15) / 16 * 16;            // columns of S^T
+    static constexpr int kPN = 2 * NP;                                       // columns of P^T and O^T: two terms
     static constexpr uint32_t kPBuf = kTile * kPN * kES;
     static constexpr uint32_t kQBuf = kSN * kRB;
     static constexpr bool kWide = !E4 && D == 128;              // 32 KB tiles: three stages
-    static constexpr int kST = kWide ? 3 : (kRB == 128 ? 5 : 8);
-    static constexpr int kPBufs = kWide && NP == 32 ? 1 : 2;
-    static constexpr int kQBufs = kWide && NP == 32 ? 1 : 2;
+    static constexpr int kKS = kWide ? 3 : (kRB == 128 ? 5 : 8);              // K stages
+    static constexpr int kVS = kWide && NP > 16 ? 2 : kKS;                    // V stages
+    static constexpr int kQBufs = kWide && NP > 16 ? 1 : 2;
     static constexpr uint32_t kOffK = 0;
-    static constexpr uint32_t kOffV = kOffK + kST * kTileB;
-    static constexpr uint32_t kOffP = kOffV + kST * kTileB;
-    static constexpr uint32_t kOffQ = kOffP + kPBufs * kPBuf;
-    static constexpr uint32_t kOffSeq = kOffQ + kQBufs * kQBuf;               // pre[B + 1], kv, n, r0
+    static constexpr uint32_t kOffV = kOffK + kKS * kTileB;
+    static constexpr uint32_t kOffP = kOffV + kVS * kTileB;
+    static constexpr uint32_t kOffQ = kOffP + 2 * kPBuf;
+    static constexpr uint32_t kOffQRaw = kOffQ + kQBufs * kQBuf;              // bf16 rows before the split
+    static constexpr uint32_t kOffSeq = kOffQRaw + (E4 ? NP * D * 2 : 0);     // pre[B + 1], kv, n, r0
     static constexpr uint32_t kOffMeta = kOffSeq + 4 * (4 * MASW_MAX_BATCH + 4);
-    static constexpr uint32_t kOffRed = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);  // [2][4][NP] floats
-    static constexpr uint32_t kOffQs = kOffRed + 2 * 4 * NP * 4;                   // scale of Q per buffer
+    static constexpr uint32_t kOffStats = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);
+    // per group: row maxima and row sums of its four warps [2][4][NP], references [NP]
+    static constexpr int kStats = 9 * NP;
+    static constexpr uint32_t kOffQs = kOffStats + 2 * kStats * 4;             // scale of Q per buffer
     static constexpr uint32_t kOffBar = kOffQs + 16;
     // barriers
-    static constexpr int kKFull = 0, kKFree = kST, kVFull = 2 * kST, kVFree = 3 * kST, kMetaBar = 4 * kST;
+    static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kMetaBar = kVFree + kVS;
     static constexpr int kSFull = kMetaBar + (E4 ? kMeta : 0), kSFree = kSFull + 2, kPFull = kSFree + 2, kPFree = kPFull + 2;
-    static constexpr int kQFull = kPFree + 2, kQFree = kQFull + 2, kDone = kQFree + 2, kBars = kDone + 2;
+    static constexpr int kQFull = kPFree + 2, kQFree = kQFull + 2, kStat = kQFree + 2, kOFree = kStat + 1, kDone = kOFree + 1, kBars = kDone + 2;
     static constexpr uint32_t kSmem = kOffBar + 8 * kBars + 16;               // + TMEM address, abort flag
     static constexpr uint32_t kColO = 2 * kSN;
-    static constexpr uint32_t kCols = 2 * kSN + kPN <= 64 ? 64 : (2 * kSN + kPN <= 128 ? 128 : 256);
+    static constexpr uint32_t kColsUsed = 2 * kSN + 2 * kPN;
+    static constexpr uint32_t kCols = kColsUsed <= 64 ? 64 : (kColsUsed <= 128 ? 128 : (kColsUsed <= 256 ? 256 : 512));
     static constexpr uint32_t kType = E4 ? 0 : 1;               // operand type field: e4m3 / bf16
     static constexpr uint32_t kBase = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(kTile >> 4) << 24);
     static constexpr uint32_t kIdescS = kBase | ((uint32_t)(kSN >> 3) << 17);
     static constexpr uint32_t kIdescO = kBase | (1u << 15) | (1u << 16) | ((uint32_t)(kPN >> 3) << 17);
     // the exponent's reference lies this far below the largest score, and may be
     // exceeded by 2^8: e4m3 weights reach 256 (of 448)
-    static constexpr float kHead = E4 ? 5.f : 0.f;
+    static constexpr float kHead = E4 ? 6.f : 0.f;
     static_assert(kSmem + 1024 <= 232448, "shared memory");
-    static_assert(kST + 2 < kMeta, "scales would be overwritten");
+    static_assert(kKS + 2 < kMeta, "scales would be overwritten");
 };
+
+// wait_or_abort in few instructions: the kernel is large, and what stalled it most
+// was fetching instructions.  try_wait itself suspends the thread for a while.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    uint32_t n = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (++n == kWaitPolls) {
+            *abort_flag = 1;
+            atomicExch(err, MASW_ETIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// N consecutive fp32 columns (a multiple of 8) of this thread's TMEM lane
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* v) {
+    if constexpr (N >= 32) {
+        tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld_cols<N - 32>(taddr + 32, v + 32);
+    } else if constexpr (N >= 16) {
+        tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
+        tmem_ld_cols<N - 16>(taddr + 16, v + 16);
+    } else if constexpr (N >= 8) {
+        tmem_ld8(taddr, *reinterpret_cast<uint32_t(*)[8]>(v));
+    }
+}
 
 // A CTA's walk over its tiles, piece by piece (a piece: tiles of one pair).
 struct Walk {
@@ -104,15 +141,26 @@ __device__ __forceinline__ bool next_piece(Walk& w, const int* pre, int B, int H
     return true;
 }
 
-__device__ __forceinline__ bool bar_or(bool x) {   // vote over the 128 softmax threads
+__device__ __forceinline__ bool bar_or(int group, bool x) {   // vote over a group's 128 threads
     uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
                  : "=r"(r)
-                 : "r"((uint32_t)x)
+                 : "r"((uint32_t)x), "r"(1 + group)
                  : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void bar_softmax() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void bar_group(int group) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+
+// The softmax groups need more registers than the launch gives a thread when they
+// hold over 16 rows: 256 x 216 + 128 x 72 = 384 x 168.
+template <int NP>
+__device__ __forceinline__ void take_registers() {
+    if constexpr (NP > 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+}
+template <int NP>
+__device__ __forceinline__ void give_registers() {
+    if constexpr (NP > 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+}
 
 __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
     uint32_t r;
@@ -148,8 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     int* s_n = s_kv + MASW_MAX_BATCH;
     int* s_r0 = s_n + MASW_MAX_BATCH;
     float4* meta = reinterpret_cast<float4*>(smem + C::kOffMeta);   // [kMeta][8]: K scale, log2 V scale, 1 / V scale
-    float* red = reinterpret_cast<float*>(smem + C::kOffRed);       // [4][NP] row maxima of the warps
-    float* sums = red + 4 * NP;                                     // [4][NP] row sums of the warps
+    float* stats = reinterpret_cast<float*>(smem + C::kOffStats);
     float* qscale = reinterpret_cast<float*>(smem + C::kOffQs);
     auto bar_at = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
     const PagedView& c = p.c;
@@ -166,9 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     }
     if (tid == 0) {
         for (int i = 0; i < C::kBars; ++i)
-            mbar_init(bars + i, i >= C::kQFree && i < C::kQFree + 2                                                         ? 5
-                                : (i >= C::kSFree && i < C::kSFree + 2) || (i >= C::kPFull && i < C::kPFull + 2) ? 4
-                                                                                                                 : 1);
+            mbar_init(bars + i, i >= C::kQFree && i < C::kQFree + 2                             ? 9
+                                : (i >= C::kSFree && i < C::kSFree + 2) || (i >= C::kPFull && i < C::kPFull + 2) ||
+                                          i == C::kStat || i == C::kOFree
+                                      ? 4
+                                      : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -192,23 +241,27 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         }
         walk.b = lo;
     }
-    auto wait = [&](int bar, int phase) { return wait_or_abort(bars + bar, (uint32_t)phase & 1u, abort_flag, err); };
+    auto wait = [&](int bar, int phase) { return wait_bounded(bars + bar, (uint32_t)phase & 1u, abort_flag, err); };
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     bool ok = true;
 
-    if (warp == 4) {
+    // one register change for each whole group of four warps
+    if (warp >= 8) {
+    give_registers<NP>();
+    if (warp == 8) {
         // ---------------- S^T = K Q^T ----------------
-        if (lane == 0) {
-            int i = 0, piece = 0;
-            while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
-                const int qb = piece % C::kQBufs;
-                ok = wait(C::kQFull + qb, piece / C::kQBufs);
-                const uint64_t bq = smem_desc(sb + C::kOffQ + qb * C::kQBuf, 128, (C::kRB / 16) * 128, 0);
-                for (int j = 0; ok && j < walk.nt; ++j, ++i) {
-                    const int st = i % C::kST, sbuf = i & 1;
-                    ok = wait(C::kKFull + st, i / C::kST) && (i < 2 || wait(C::kSFree + sbuf, i / 2 - 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t ak = smem_desc(sb + C::kOffK + st * C::kTileB, 16, C::kAtom, C::kSwz);
+        int i = 0, piece = 0;
+        while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
+            const int qb = piece % C::kQBufs;
+            ok = all(wait(C::kQFull + qb, piece / C::kQBufs));
+            const uint64_t bq = smem_desc(sb + C::kOffQ + qb * C::kQBuf, 128, (C::kRB / 16) * 128, 0);
+            for (int j = 0; ok && j < walk.nt; ++j, ++i) {
+                const int st = i % C::kKS, sbuf = i & 1;
+                ok = all(wait(C::kKFull + st, i / C::kKS)) && (i < 2 || all(wait(C::kSFree + sbuf, i / 2 - 1)));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ak = smem_desc(sb + C::kOffK + st * C::kTileB, 16, C::kAtom, C::kSwz);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < C::kRB / 32; ++kk) {
                         const uint64_t a = ak + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
@@ -220,52 +273,58 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     umma_commit(bar_at(C::kKFree + st));
                     if (j + 1 == walk.nt) umma_commit(bar_at(C::kQFree + qb));
                 }
-                ++piece;
+                __syncwarp();
             }
-            // nothing may arrive on a barrier after the CTA ended
-            if (ok && i > 0) ok = wait(C::kKFree + (i - 1) % C::kST, (i - 1) / C::kST) && wait(C::kQFree + (piece - 1) % C::kQBufs, (piece - 1) / C::kQBufs);
-            if (!ok) {   // let the matrix products in flight end before the CTA does
-                *abort_flag = 1;
-                umma_commit(bar_at(C::kDone));
-                mbar_wait(bars + C::kDone, 0, nullptr);
-            }
+            ++piece;
+        }
+        // nothing may arrive on a barrier after the CTA ended
+        if (ok && i > 0)
+            ok = all(wait(C::kKFree + (i - 1) % C::kKS, (i - 1) / C::kKS)) &&
+                 all(wait(C::kQFree + (piece - 1) % C::kQBufs, (piece - 1) / C::kQBufs));
+        if (!ok) {   // let the matrix products in flight end before the CTA does
+            *abort_flag = 1;
+            if (elect_one()) umma_commit(bar_at(C::kDone));
+            __syncwarp();
+            mbar_wait(bars + C::kDone, 0, nullptr);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         // ---------------- O^T += V^T P^T ----------------
-        if (lane == 0) {
-            int i = 0;
-            while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
-                for (int j = 0; ok && j < walk.nt; ++j, ++i) {
-                    const int st = i % C::kST, pb = i % C::kPBufs;
-                    ok = wait(C::kPFull + pb, i / C::kPBufs) && wait(C::kVFull + st, i / C::kST);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // head_dim 64: the second half of the 128 M rows repeats the first
-                    // (a leading offset of 0); head_dim 128 in bf16: the second panel
-                    const uint64_t av = smem_desc(sb + C::kOffV + st * C::kTileB, C::kPanels == 2 ? C::kPanel : 0, C::kAtom, C::kSwz);
-                    const uint64_t bp = smem_desc(sb + C::kOffP + pb * C::kPBuf, 128, 2048, 0);
-                    constexpr int kKeys = 32 / C::kES;   // keys of one matrix instruction
+        int i = 0;
+        while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
+            for (int j = 0; ok && j < walk.nt; ++j, ++i) {
+                const int st = i % C::kVS, pb = i & 1;
+                ok = all(wait(C::kPFull + pb, i / 2)) && all(wait(C::kVFull + st, i / C::kVS));
+                if (!ok) break;
+                tc_fence_after();
+                // head_dim 64: the second half of the 128 M rows repeats the first
+                // (a leading offset of 0); head_dim 128 in bf16: the second panel
+                const uint64_t av = smem_desc(sb + C::kOffV + st * C::kTileB, C::kPanels == 2 ? C::kPanel : 0, C::kAtom, C::kSwz);
+                const uint64_t bp = smem_desc(sb + C::kOffP + pb * C::kPBuf, 128, 2048, 0);
+                constexpr int kKeys = 32 / C::kES;   // keys of one matrix instruction
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / kKeys; ++kk) {
                         const uint64_t a = av + (uint64_t)((kk * kKeys * C::kPB) >> 4);
                         const uint64_t b = bp + (uint64_t)((kk * kKeys * 16) >> 4);
-                        if (E4) umma_f8(tmem + C::kColO, a, b, C::kIdescO, j > 0 || kk > 0);
-                        else umma_bf16(tmem + C::kColO, a, b, C::kIdescO, j > 0 || kk > 0);
+                        if (E4) umma_f8(tmem + C::kColO + pb * C::kPN, a, b, C::kIdescO, j > 1 || kk > 0);
+                        else umma_bf16(tmem + C::kColO + pb * C::kPN, a, b, C::kIdescO, j > 1 || kk > 0);
                     }
                     umma_commit(bar_at(C::kPFree + pb));
                     umma_commit(bar_at(C::kVFree + st));
                 }
-            }
-            if (ok && i > 0) ok = wait(C::kVFree + (i - 1) % C::kST, (i - 1) / C::kST);
-            if (!ok) {
-                *abort_flag = 1;
-                umma_commit(bar_at(C::kDone + 1));
-                mbar_wait(bars + C::kDone + 1, 0, nullptr);
+                __syncwarp();
             }
         }
+        if (ok && i > 0) ok = all(wait(C::kVFree + (i - 1) % C::kVS, (i - 1) / C::kVS));
+        if (!ok) {
+            *abort_flag = 1;
+            if (elect_one()) umma_commit(bar_at(C::kDone + 1));
+            __syncwarp();
+            mbar_wait(bars + C::kDone + 1, 0, nullptr);
+        }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == 10) {
         // ---------------- page ids, scales, TMA ----------------
         // A lane holds the page of one box (at most 128 rows of a page); a batch
         // is up to 32 boxes of a piece.  The next batch's page ids are loaded
@@ -273,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         const int box = imin(c.P, kTile), bpt = kTile / box, bt = 32 / bpt;   // boxes a tile, tiles a batch
         Walk w = walk;
         int left = 0, at = 0;            // tiles of the piece not yet in a batch, and the first of them
-        struct Batch { int h, tile, nt, pid; bool in; float ks, vs; };
+        struct Batch { int h, tile, nt, pid, lo, hi; bool in; float ks, lvs, ivs; };   // boxes [lo, hi) hold visible keys
         auto next_batch = [&](Batch& x) {
             x.nt = 0;
             x.in = false;
@@ -288,19 +347,26 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             at += x.nt;
             left -= x.nt;
             const TileRange r = tile_range(s_n[w.b], s_kv[w.b], p.window);
-            const int key = x.tile * kTile + lane * box;
-            x.in = lane < x.nt * bpt && key < r.hi && (key / c.P + 1) * c.P > r.lo;
-            x.pid = x.in ? __ldg(c.table + (size_t)w.b * c.table_stride + key / c.P) : 0;
+            const int key0 = x.tile * kTile;
+            x.lo = imax(0, r.lo / c.P * c.P - key0) / box;   // pages wholly before the first visible key are left out
+            x.hi = imin(x.nt * bpt, (r.hi - key0 + box - 1) / box);
+            x.in = lane >= x.lo && lane < x.hi;
+            x.pid = x.in ? __ldg(c.table + (size_t)w.b * c.table_stride + (key0 + lane * box) / c.P) : 0;
         };
         auto check_and_scale = [&](Batch& x) {
             if (x.in && (x.pid < 0 || x.pid >= c.n_pages)) {
                 atomicExch(err, MASW_EINVAL);
                 x.pid = 0;
             }
-            x.ks = x.vs = 1.f;
-            if (E4 && x.in) {
-                x.ks = __ldg(c.k_scale + (size_t)x.pid * Hkv + x.h);
-                x.vs = __ldg(c.v_scale + (size_t)x.pid * Hkv + x.h);
+            if (E4) {
+                float vs = 1.f;
+                x.ks = 1.f;
+                if (x.in) {
+                    x.ks = __ldg(c.k_scale + (size_t)x.pid * Hkv + x.h);
+                    vs = __ldg(c.v_scale + (size_t)x.pid * Hkv + x.h);
+                }
+                x.lvs = vs == 1.f ? 0.f : __log2f(vs);
+                x.ivs = __frcp_rn(vs);
             }
         };
         Batch cur, nxt;
@@ -313,95 +379,114 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             Batch nn;
             next_batch(nn);
             for (int j = 0; ok && j < cur.nt; ++j, ++i) {
-                const int st = i % C::kST;
-                const bool mine = lane / bpt == j && cur.in;
-                const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-                const uint32_t bytes = (uint32_t)boxes * box * C::kRB;
-                const int row = ((cur.tile + j) * kTile + (lane % bpt) * box) & (c.P - 1);
-                const uint32_t dst = (uint32_t)st * C::kTileB + (uint32_t)((lane % bpt) * box * C::kPB);
-                if (i >= C::kST) ok = __all_sync(0xffffffffu, wait(C::kKFree + st, i / C::kST - 1));
+                const int ks = i % C::kKS, vs = i % C::kVS;
+                const int b0 = imax(cur.lo, j * bpt), b1 = imin(cur.hi, (j + 1) * bpt);   // the tile's boxes
+                const uint32_t bytes = (uint32_t)(imax(0, b1 - b0) * box * C::kRB);
+                auto load = [&](const CUtensorMap* map, uint32_t tile, int bar) {
+                    // the whole warp walks the boxes, one lane issues
+                    for (int q = b0; q < b1; ++q) {
+                        const int pid = __shfl_sync(0xffffffffu, cur.pid, q);
+                        const int row = (cur.tile * kTile + q * box) & (c.P - 1);
+                        const uint32_t dst = tile + (uint32_t)((q - j * bpt) * box * C::kPB);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int pn = 0; pn < C::kPanels; ++pn)
+                                tma_load_4d(dst + pn * C::kPanel, map, pn * C::kPB / C::kES, row, cur.h, pid, bar_at(bar));
+                        }
+                    }
+                    __syncwarp();
+                };
+                if (i >= C::kKS) ok = all(wait(C::kKFree + ks, i / C::kKS - 1));
                 if (!ok) break;
-                if (E4 && lane / bpt == j)
-                    meta[(i % kMeta) * 8 + lane % bpt] =
-                        make_float4(cur.ks, cur.vs == 1.f ? 0.f : __log2f(cur.vs), __frcp_rn(cur.vs), 0.f);
-                __syncwarp();
-                if (lane == 0) {
+                if (E4) {
+                    if (lane / bpt == j) meta[(i % kMeta) * 8 + lane % bpt] = make_float4(cur.ks, cur.lvs, cur.ivs, 0.f);
+                    __syncwarp();
+                }
+                if (elect_one()) {
                     if (E4) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
-                    mbar_expect_tx(bars + C::kKFull + st, bytes);
+                    mbar_expect_tx(bars + C::kKFull + ks, bytes);
                 }
                 __syncwarp();
-                if (mine)
-#pragma unroll
-                    for (int pn = 0; pn < C::kPanels; ++pn)
-                        tma_load_4d(sb + C::kOffK + dst + pn * C::kPanel, &p.tm_k, pn * C::kPB / C::kES, row, cur.h, cur.pid,
-                                    bar_at(C::kKFull + st));
-                if (i >= C::kST) ok = __all_sync(0xffffffffu, wait(C::kVFree + st, i / C::kST - 1));
+                load(&p.tm_k, sb + C::kOffK + ks * C::kTileB, C::kKFull + ks);
+                if (i >= C::kVS) ok = all(wait(C::kVFree + vs, i / C::kVS - 1));
                 if (!ok) {   // the K tile was issued, its V tile was not
-                    mbar_wait(bars + C::kKFull + st, (uint32_t)(i / C::kST) & 1u, nullptr);
+                    mbar_wait(bars + C::kKFull + ks, (uint32_t)(i / C::kKS) & 1u, nullptr);
                     break;
                 }
-                if (lane == 0) mbar_expect_tx(bars + C::kVFull + st, bytes);
+                if (elect_one()) mbar_expect_tx(bars + C::kVFull + vs, bytes);
                 __syncwarp();
-                if (mine)
-#pragma unroll
-                    for (int pn = 0; pn < C::kPanels; ++pn)
-                        tma_load_4d(sb + C::kOffV + dst + pn * C::kPanel, &p.tm_v, pn * C::kPB / C::kES, row, cur.h, cur.pid,
-                                    bar_at(C::kVFull + st));
+                load(&p.tm_v, sb + C::kOffV + vs * C::kTileB, C::kVFull + vs);
             }
             cur = nxt;
             nxt = nn;
         }
         // after a wait gave up, and at the end: no copy may be in flight when the CTA ends
         if (!ok) *abort_flag = 1;
-        for (int k = imax(0, i - C::kST); k < i; ++k) {
-            mbar_wait(bars + C::kKFull + k % C::kST, (uint32_t)(k / C::kST) & 1u, nullptr);
-            mbar_wait(bars + C::kVFull + k % C::kST, (uint32_t)(k / C::kST) & 1u, nullptr);
-        }
+        for (int k = imax(0, i - C::kKS); k < i; ++k)
+            mbar_wait(bars + C::kKFull + k % C::kKS, (uint32_t)(k / C::kKS) & 1u, nullptr);
+        for (int k = imax(0, i - C::kVS); k < i; ++k)
+            mbar_wait(bars + C::kVFull + k % C::kVS, (uint32_t)(k / C::kVS) & 1u, nullptr);
         __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == 11) {
         // ---------------- Q of the next pair ----------------
-        constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPass = NP / kPer;   // lanes a row, rows a pass
+        // 16-byte chunks: a row is kLanes of them, a pass kPer rows; every lane
+        // splits the chunks that it copied itself
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPass = NP / kPer;
+        const int e0 = (lane % kLanes) * 8, rl = lane / kLanes;
         int piece = 0;
         while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
             const int nq = s_n[walk.b] * G, r0 = s_r0[walk.b];
-            uint4 x[kPass];
-            float amax = 0.f;
+            const int qb = piece % C::kQBufs;
+            const uint32_t qbase = sb + C::kOffQ + qb * C::kQBuf;
+            // K-major core matrices of 8 rows x 16 bytes, consecutive along the row
+            auto at = [&](int row, int byte) {
+                return qbase + (uint32_t)((row >> 3) * (C::kRB / 16) * 128 + (byte >> 4) * 128 + (row & 7) * 16 + (byte & 15));
+            };
+            const uint32_t raw = sb + C::kOffQRaw + (uint32_t)lane * 16u;   // pass s: 512 bytes further
+            if (!E4 && piece >= C::kQBufs) ok = all(wait(C::kQFree + qb, piece / C::kQBufs - 1));
+            if (!ok) break;
+            int tok = rl / G, g = rl - tok * G;
 #pragma unroll
             for (int s = 0; s < kPass; ++s) {
-                const int r = s * kPer + lane / kLanes;
-                x[s] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < nq)
-                    x[s] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(r0 + r / G) * p.q_stride +
-                                                                (size_t)(walk.h * G + r % G) * D) +
-                                 lane % kLanes);
+                const int r = s * kPer + rl;
+                const bool in = r < nq;
+                const __nv_bfloat16* src = p.q + (size_t)(r0 + (in ? tok : 0)) * p.q_stride + (size_t)(walk.h * G + (in ? g : 0)) * D + e0;
+                if (E4) {
+                    cp_async16(raw + s * 512, src, in ? 16 : 0);
+                } else {
+                    cp_async16(at(r, e0 * 2), src, in ? 16 : 0);
+                    if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
+                }
+                g += kPer;
+                while (g >= G) {
+                    g -= G;
+                    ++tok;
+                }
             }
-            const int qb = piece % C::kQBufs;
+            cp_async_commit();
+            cp_async_wait<0>();
             float inv = 1.f;
-            if (E4) {
+            if constexpr (E4) {
+                float amax = 0.f;
 #pragma unroll
                 for (int s = 0; s < kPass; ++s) {
+                    const float4 v = ld_shared_v4f(raw + s * 512);
                     float f[8];
-                    Elem<__nv_bfloat16>::unpack(x[s], f);
+                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
                 }
 #pragma unroll
                 for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 inv = 1.f / pow2_scale(amax);
-            }
-            if (piece >= C::kQBufs) ok = __all_sync(0xffffffffu, wait(C::kQFree + qb, piece / C::kQBufs - 1));
-            if (!ok) break;
-            const uint32_t qbase = sb + C::kOffQ + qb * C::kQBuf;
-            // K-major core matrices of 8 rows x 16 bytes, consecutive along the row
-            auto at = [&](int row, int byte) {
-                return qbase + (uint32_t)((row >> 3) * (C::kRB / 16) * 128 + (byte >> 4) * 128 + (row & 7) * 16 + (byte & 15));
-            };
+                if (piece >= C::kQBufs) ok = all(wait(C::kQFree + qb, piece / C::kQBufs - 1));
+                if (!ok) break;
 #pragma unroll
-            for (int s = 0; s < kPass; ++s) {
-                const int r = s * kPer + lane / kLanes, e0 = (lane % kLanes) * 8;
-                if (E4) {
+                for (int s = 0; s < kPass; ++s) {
+                    const int r = s * kPer + rl;
+                    const float4 v = ld_shared_v4f(raw + s * 512);
                     float f[8];
-                    Elem<__nv_bfloat16>::unpack(x[s], f);
+                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
                     uint32_t w1[4], w2[4];
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
@@ -412,11 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                         w1[e / 2] = q1;
                         w2[e / 2] = e4m3x2((a - a1) * 16.f, (b - b1) * 16.f);
                     }
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(r, e0)), "r"(w1[0] | (w1[1] << 16)), "r"(w1[2] | (w1[3] << 16)) : "memory");
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(NP + r, e0)), "r"(w2[0] | (w2[1] << 16)), "r"(w2[2] | (w2[3] << 16)) : "memory");
-                } else {
-                    st_shared_v4(at(r, e0 * 2), x[s].x, x[s].y, x[s].z, x[s].w);
-                    if (NP < 16) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
+                    st_shared_v2(at(r, e0), w1[0] | (w1[1] << 16), w1[2] | (w1[3] << 16));
+                    st_shared_v2(at(NP + r, e0), w2[0] | (w2[1] << 16), w2[2] | (w2[3] << 16));
                 }
             }
             if (lane == 0) qscale[qb] = p.scale_log2 / inv;
@@ -426,13 +508,21 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             ++piece;
         }
         if (!ok) *abort_flag = 1;
+    }
     } else {
-        // ---------------- softmax: thread tid owns key tid of each tile ----------------
+        take_registers<NP>();
+        // ---------------- softmax: thread wt of a group owns key wt of the group's tiles ----------------
         // After a wait gave up these warps go on to the end of their tiles (every
         // later wait returns at once), so that they meet at their barriers.
-        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        const uint32_t t_o = tmem + C::kColO + lane_off;
-        int i = 0, piece = 0;
+        const int group = warp >> 2, wt = tid & 127, gw = warp & 3;
+        const uint32_t lane_off = (uint32_t)(gw * 32) << 16;
+        const uint32_t t_s = tmem + group * C::kSN + lane_off;
+        const uint32_t t_o = tmem + C::kColO + lane_off;             // group 0's; group 1's kPN columns further
+        const uint32_t t_own = t_o + group * C::kPN;
+        float* red = stats + group * C::kStats;                     // [4][NP] row maxima of the group's warps
+        float* sums = red + 4 * NP;                                  // [4][NP] row sums
+        float* ref = sums + 4 * NP;                                  // [NP] references
+        int i0 = 0, piece = 0;
         bool first = true;
         while (next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
             const int b = walk.b, n = s_n[b], kv = s_kv[b], nq = n * G, q_pos = kv - n;
@@ -440,51 +530,31 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             const int qb = piece % C::kQBufs;
             // keys that every row sees: [all_lo, all_hi)
             const int all_hi = q_pos + 1, all_lo = p.window > 0 ? imax(0, kv - p.window) : 0;
+            // rows without a reference yet, because they have seen no key (the same in
+            // every thread of the group)
+            uint32_t unset = nq == 32 ? 0xffffffffu : (1u << nq) - 1u;
             float mref[NP], l[NP];
 #pragma unroll
-            for (int r = 0; r < NP; ++r) {
-                mref[r] = -1e30f;
-                l[r] = 0.f;
-            }
-            ok &= __all_sync(0xffffffffu, wait(C::kQFull + qb, piece / C::kQBufs)) != 0;
+            for (int r = 0; r < NP; ++r) mref[r] = l[r] = 0.f;
+            ok &= wait(C::kQFull + qb, piece / C::kQBufs);
             const float qs = qscale[qb];
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_at(C::kQFree + qb));
-            for (int j = 0; j < walk.nt; ++j, ++i) {
-                const int sbuf = i & 1;
-                ok &= __all_sync(0xffffffffu, wait(C::kSFull + sbuf, i / 2)) != 0;
-                tc_fence_after();
-                float x[NP];
-                {
-                    uint32_t sv[C::kSN];
-                    const uint32_t ts = tmem + sbuf * C::kSN + lane_off;
-                    if constexpr (C::kSN == 16) {
-                        tmem_ld16(ts, sv);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < C::kSN / 32; ++q)
-                            tmem_ld32(ts + q * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + q * 32));
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int r = 0; r < NP; ++r)
-                        x[r] = E4 ? fmaf(__uint_as_float(sv[NP + r]), 0.0625f, __uint_as_float(sv[r])) : __uint_as_float(sv[r]);
-                }
+            bool o_free = group == 0 || piece == 0;   // group 0 has read this group's O and sums of the last piece
+            for (int j = (i0 ^ group) & 1; j < walk.nt; j += 2) {
+                const int i = i0 + j, turn = i >> 1;
+                const int tile0 = (walk.tile + j) * kTile, key = tile0 + wt;
+                const bool masked = tile0 < all_lo || tile0 + kTile > all_hi;
+                const bool seen = key >= range.lo && key < range.hi;   // by some row
+                uint32_t see = 0xffffffffu;                            // by which rows
                 float ks = qs, lvs = 0.f, ivs = 1.f;
-                const int tile0 = (walk.tile + j) * kTile, key = tile0 + tid;
                 if (E4) {
-                    ok &= __all_sync(0xffffffffu, wait(C::kMetaBar + i % kMeta, i / kMeta)) != 0;
-                    const float4 mt = meta[(i % kMeta) * 8 + (c.P >= kTile ? 0 : tid / c.P)];
+                    ok &= wait(C::kMetaBar + i % kMeta, i / kMeta);
+                    const float4 mt = meta[(i % kMeta) * 8 + (c.P >= kTile ? 0 : wt / c.P)];
                     ks *= mt.x;
                     lvs = mt.y;
                     ivs = mt.z;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_at(C::kSFree + sbuf));
-                const bool masked = tile0 < all_lo || tile0 + kTile > all_hi;
-                const bool seen = key >= range.lo && key < range.hi;   // by some row
-                uint32_t see = 0xffffffffu;                            // by which rows
                 if (masked) {
                     if (!seen) {
                         ks = 1.f;
@@ -501,181 +571,227 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                         }
                     }
                     // a V row that no row sees must not reach the product
-                    const int st = i % C::kST;
-                    ok &= __all_sync(0xffffffffu, wait(C::kVFull + st, i / C::kST)) != 0;
+                    const int st = i % C::kVS;
+                    ok &= wait(C::kVFull + st, i / C::kVS);
                     if (!seen) {
 #pragma unroll
                         for (int pn = 0; pn < C::kPanels; ++pn)
 #pragma unroll
                             for (int q = 0; q < C::kPB / 16; ++q)
-                                st_shared_v4(sb + C::kOffV + st * C::kTileB + pn * C::kPanel + tid * C::kPB + q * 16, 0u, 0u, 0u, 0u);
+                                st_shared_v4(sb + C::kOffV + st * C::kTileB + pn * C::kPanel + wt * C::kPB + q * 16, 0u, 0u, 0u, 0u);
                     }
                 }
-                // weights relative to the reference of each row; the reference moves
-                // when a score exceeds it by more than 2^8
-                float mx = -INFINITY;
+                ok &= wait(C::kSFull + group, turn);
+                __syncwarp();
+                tc_fence_after();
+                // a: this key's scores of all rows in the log2 domain (the V scale with
+                // them) relative to the rows' references; -inf where a row does not see
+                // the key.  A reference moves when a score exceeds it by more than 2^8,
+                // and O and the sums shrink with it; then a is computed anew.
                 float a[NP];
+                bool p_free = turn == 0;
+#pragma unroll 1
+                for (;;) {
+                    {
+                        uint32_t sv[E4 ? 2 * NP : NP];
+                        tmem_ld_cols<E4 ? 2 * NP : NP>(t_s, sv);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < NP; ++r) {
-                    a[r] = fmaf(x[r], ks, lvs - mref[r]);
-                    if (masked) a[r] = (see >> r) & 1u ? a[r] : -INFINITY;
-                    mx = fmaxf(mx, a[r]);
-                }
-                if (bar_or(mx > 8.f)) {
+                        for (int r = 0; r < NP; ++r) {
+                            const float x = E4 ? fmaf(__uint_as_float(sv[NP + r]), 0.0625f, __uint_as_float(sv[r])) : __uint_as_float(sv[r]);
+                            a[r] = fmaf(x, ks, lvs - mref[r]);
+                        }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int r = 0; r < NP; ++r) a[r] = (see >> r) & 1u ? a[r] : -INFINITY;
+                    }
+                    float mx = a[0];
+#pragma unroll
+                    for (int r = 1; r < NP; ++r) mx = fmaxf(mx, a[r]);
+                    bool move = mx > 8.f;
+                    if (unset) {
+#pragma unroll
+                        for (int r = 0; r < NP; ++r) move = move || (((unset >> r) & 1u) && a[r] > -3e38f);
+                    }
+                    if (!bar_or(group, move)) break;
 #pragma unroll
                     for (int r = 0; r < NP; ++r) {
-                        float s = (see >> r) & 1u ? fmaf(x[r], ks, lvs) : -INFINITY;
+                        float s = a[r];
 #pragma unroll
                         for (int o = 16; o; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-                        if (lane == 0) red[warp * NP + r] = s;
+                        if (lane == 0) red[gw * NP + r] = s;
                     }
-                    bar_softmax();
-                    if (j > 0) {
-                        // O holds tiles 0..j-1 of the piece once the last product is done
-                        const int pb = (i - 1) % C::kPBufs;
-                        ok &= __all_sync(0xffffffffu, wait(C::kPFree + pb, (i - 1) / C::kPBufs)) != 0;
+                    bar_group(group);
+                    if (j > 1 && !p_free) {
+                        // O holds the group's earlier tiles of the piece once the last product is done
+                        ok &= wait(C::kPFree + group, turn - 1);
+                        __syncwarp();
                         tc_fence_after();
+                        p_free = true;
                     }
-                    float alpha[NP];
+                    uint32_t now_set = 0u;
 #pragma unroll
                     for (int r = 0; r < NP; ++r) {
-                        const float top = fmaxf(fmaxf(red[r], red[NP + r]), fmaxf(red[2 * NP + r], red[3 * NP + r])) - C::kHead;
-                        const float nm = fmaxf(mref[r], top);
-                        alpha[r] = ex2_approx(mref[r] - nm);
-                        l[r] *= alpha[r];
-                        mref[r] = nm;
-                        a[r] = (see >> r) & 1u ? fmaf(x[r], ks, lvs - nm) : -INFINITY;
+                        const float top = fmaxf(fmaxf(red[r], red[NP + r]), fmaxf(red[2 * NP + r], red[3 * NP + r]));
+                        const bool fresh = (unset >> r) & 1u;
+                        const float up = fresh ? (top > -3e38f ? top - C::kHead : 0.f) : fmaxf(0.f, top - C::kHead);
+                        mref[r] += up;
+                        a[r] = fresh ? 1.f : ex2_approx(-up);   // what the sums and O shrink by
+                        l[r] *= a[r];
+                        if (top > -3e38f) now_set |= 1u << r;
                     }
-                    if (j > 0) {
+                    unset &= ~now_set;
+                    if (j > 1) {
 #pragma unroll
-                        for (int q = 0; q < C::kPN / 16; ++q) {
-                            uint32_t ov[16];
-                            tmem_ld16(t_o + q * 16, ov);
+                        for (int q = 0; q < C::kPN / 8; ++q) {
+                            uint32_t ov[8];
+                            tmem_ld8(t_own + q * 8, ov);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha[(q * 16 + e) % NP]);
-                            tmem_st16(t_o + q * 16, ov);
+                            for (int e = 0; e < 8; ++e)
+                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * a[(q * 8 + e) % NP]);
+                            tmem_st8(t_own + q * 8, ov);
                         }
                         tmem_wait_st();
                     }
+                    bar_group(group);   // the maxima were read
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_at(C::kSFree + group));
 #pragma unroll
                 for (int r = 0; r < NP; ++r) {
                     a[r] = ex2_approx(a[r]);
                     l[r] = fmaf(a[r], ivs, l[r]);
                 }
-                const int pb = i % C::kPBufs;
-                if (i >= C::kPBufs) {
-                    ok &= __all_sync(0xffffffffu, wait(C::kPFree + pb, i / C::kPBufs - 1)) != 0;
-                    tc_fence_after();
-                }
-                // this key's weights of all rows: the terms side by side, in 16-byte
-                // chunks of core matrices (8 keys x 16 bytes)
-                const uint32_t pw = sb + C::kOffP + pb * C::kPBuf + (uint32_t)((tid >> 3) * 128 + (tid & 7) * 16);
+                if (!p_free) ok &= wait(C::kPFree + group, turn - 1);
+                // this key's weights of all rows, first terms then second ones, in
+                // 16-byte chunks of core matrices (8 keys x 16 bytes)
+                const uint32_t pw = sb + C::kOffP + group * C::kPBuf + (uint32_t)((wt >> 3) * 128 + (wt & 7) * 16);
+                uint32_t w[C::kPN * C::kES / 4];
                 if constexpr (E4) {
-                    uint32_t w[3][NP / 4];
 #pragma unroll
                     for (int r = 0; r < NP; r += 4) {
-                        uint32_t h0 = cvt_f16x2(a[r], a[r + 1]), h1 = cvt_f16x2(a[r + 2], a[r + 3]);
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            const uint32_t e0 = cvt_e4m3x2_f16x2(h0), e1 = cvt_e4m3x2_f16x2(h1);
-                            w[k][r / 4] = e0 | (e1 << 16);
-                            if (k < 2) {
-                                h0 = rest16(h0, e4m3x2_to_f16x2(e0));
-                                h1 = rest16(h1, e4m3x2_to_f16x2(e1));
-                            }
-                        }
-                    }
-                    if constexpr (NP == 8) {
-                        st_shared_v4(pw, w[0][0], w[0][1], w[1][0], w[1][1]);
-                        st_shared_v4(pw + 2048, w[2][0], w[2][1], 0u, 0u);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 3; ++k)
-#pragma unroll
-                            for (int q = 0; q < NP / 16; ++q)
-                                st_shared_v4(pw + (k * (NP / 16) + q) * 2048, w[k][4 * q], w[k][4 * q + 1], w[k][4 * q + 2], w[k][4 * q + 3]);
+                        const uint32_t h0 = cvt_f16x2(a[r], a[r + 1]), h1 = cvt_f16x2(a[r + 2], a[r + 3]);
+                        const uint32_t e0 = cvt_e4m3x2_f16x2(h0), e1 = cvt_e4m3x2_f16x2(h1);
+                        w[r / 4] = e0 | (e1 << 16);
+                        w[NP / 4 + r / 4] = cvt_e4m3x2_f16x2(rest16(h0, e4m3x2_to_f16x2(e0))) |
+                                            (cvt_e4m3x2_f16x2(rest16(h1, e4m3x2_to_f16x2(e1))) << 16);
                     }
                 } else {
 #pragma unroll
-                    for (int r = 0; r < NP; r += 8) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float u = a[r + 2 * e], v = a[r + 2 * e + 1];
-                            hi[e] = pack_bf16(u, v);
-                            lo[e] = pack_bf16(u - bf16lo(hi[e]), v - bf16hi(hi[e]));
-                        }
-                        st_shared_v4(pw + (r / 8) * 2048, hi[0], hi[1], hi[2], hi[3]);
-                        st_shared_v4(pw + (NP / 8 + r / 8) * 2048, lo[0], lo[1], lo[2], lo[3]);
+                    for (int r = 0; r < NP; r += 2) {
+                        w[r / 2] = pack_bf16(a[r], a[r + 1]);
+                        w[NP / 2 + r / 2] = pack_bf16(a[r] - bf16lo(w[r / 2]), a[r + 1] - bf16hi(w[r / 2]));
                     }
+                }
+#pragma unroll
+                for (int q = 0; q < C::kPN * C::kES / 16; ++q)
+                    st_shared_v4(pw + q * 2048, w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                if (!o_free) {
+                    ok &= wait(C::kOFree, piece - 1);
+                    o_free = true;
                 }
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_at(C::kPFull + pb));
+                if (lane == 0) mbar_arrive(bar_at(C::kPFull + group));
             }
-            // the pair's (or piece's) sums over all keys, then O
+            // the piece's sums over the group's keys
 #pragma unroll
             for (int r = 0; r < NP; ++r) {
 #pragma unroll
                 for (int o = 16; o; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-                if (lane == 0) sums[warp * NP + r] = l[r];
             }
-            bar_softmax();
+            if (!o_free) ok &= wait(C::kOFree, piece - 1);
 #pragma unroll
-            for (int r = 0; r < NP; ++r) l[r] = sums[r] + sums[NP + r] + sums[2 * NP + r] + sums[3 * NP + r];
-            ok &= __all_sync(0xffffffffu, wait(C::kPFree + (i - 1) % C::kPBufs, (i - 1) / C::kPBufs)) != 0;
-            tc_fence_after();
-            float o[NP];
-            {
-                uint32_t ov[C::kPN];
-#pragma unroll
-                for (int q = 0; q < C::kPN / 16; ++q) tmem_ld16(t_o + q * 16, *reinterpret_cast<uint32_t(*)[16]>(ov + q * 16));
-                tmem_wait_ld();
-#pragma unroll
-                for (int r = 0; r < NP; ++r) {
-                    o[r] = __uint_as_float(ov[r]);
-                    if (E4)
-                        o[r] += fmaf(__uint_as_float(ov[2 * NP + r]), 0.00390625f, 0.0625f * __uint_as_float(ov[NP + r]));
-                    else
-                        o[r] += __uint_as_float(ov[NP + r]);
-                }
+            for (int r = 0; r < NP; ++r) {
+                if (lane == 0) sums[gw * NP + r] = l[r];
+                if (wt == 0) ref[r] = (unset >> r) & 1u ? -1e30f : mref[r];
             }
-            tc_fence_before();
-            if (walk.whole) {
-                int tok = s_r0[b], g = 0;
-#pragma unroll
-                for (int r = 0; r < NP; ++r) {
-                    if (r < nq) {
-                        const size_t row = (size_t)tok * p.Hq + walk.h * G + g;
-                        if (tid < D) store_out(p, row * D + tid, l[r] == 0.f ? 0.f : o[r] / l[r]);
-                        if (tid == 0 && p.lse)
-                            p.lse[row] = l[r] == 0.f ? -INFINITY : (mref[r] + __log2f(l[r])) * 0.6931471805599453f;
-                        if (++g == G) {
-                            g = 0;
-                            ++tok;
-                        }
-                    }
-                }
+            const int i1 = i0 + walk.nt;
+            if (group == 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_at(C::kStat));
             } else {
-                float* part = p.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRowsMax * (D + 2);
+                // join the two groups' sums and O (group g's last tile before i1: the
+                // one or two in the piece)
+                bar_group(group);
+                ok &= wait(C::kStat, piece);
+                const float* other = stats + C::kStats;
+                const bool had0 = walk.nt > 1 || !(i0 & 1), had1 = walk.nt > 1 || (i0 & 1);
+                if (had0) ok &= wait(C::kPFree, (i1 - 1) >> 1);
+                if (had1) ok &= wait(C::kPFree + 1, (i1 - 2) >> 1);
+                __syncwarp();
+                tc_fence_after();
+                float o[NP];
+                {
+                    float w0[NP], w1[NP];
 #pragma unroll
-                for (int r = 0; r < NP; ++r) {
-                    if (r < nq) {
-                        if (tid < D) __stcg(part + r * D + tid, o[r]);
-                        if (tid == 0) {
-                            __stcg(part + kRowsMax * D + r, l[r] == 0.f ? -INFINITY : mref[r]);
-                            __stcg(part + kRowsMax * (D + 1) + r, l[r]);
+                    for (int r = 0; r < NP; ++r) {
+                        const float m0 = ref[r], m1 = other[8 * NP + r], m = fmaxf(m0, m1);
+                        const float l0 = sums[r] + sums[NP + r] + sums[2 * NP + r] + sums[3 * NP + r];
+                        const float l1 = other[4 * NP + r] + other[5 * NP + r] + other[6 * NP + r] + other[7 * NP + r];
+                        w0[r] = ex2_approx(m0 - m);
+                        w1[r] = ex2_approx(m1 - m);
+                        l[r] = l0 * w0[r] + l1 * w1[r];
+                        mref[r] = m;
+                        o[r] = 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float f = E4 && k == 1 ? 0.0625f : 1.f;
+#pragma unroll
+                        for (int q = 0; q < NP / 8; ++q) {
+                            uint32_t u[8], v[8];
+                            tmem_ld8(t_o + k * NP + q * 8, u);
+                            tmem_ld8(t_o + C::kPN + k * NP + q * 8, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int r = q * 8 + e;
+                                if (had0) o[r] = fmaf(__uint_as_float(u[e]), f * w0[r], o[r]);
+                                if (had1) o[r] = fmaf(__uint_as_float(v[e]), f * w1[r], o[r]);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                bar_group(group);   // the sums were read
+                if (lane == 0) mbar_arrive(bar_at(C::kOFree));
+                if (walk.whole) {
+                    int tok = s_r0[b], g = 0;
+#pragma unroll
+                    for (int r = 0; r < NP; ++r) {
+                        if (r < nq) {
+                            const size_t row = (size_t)tok * p.Hq + walk.h * G + g;
+                            if (wt < D) store_out(p, row * D + wt, l[r] == 0.f ? 0.f : o[r] / l[r]);
+                            if (wt == 0 && p.lse)
+                                p.lse[row] = l[r] == 0.f ? -INFINITY : (mref[r] + __log2f(l[r])) * 0.6931471805599453f;
+                            if (++g == G) {
+                                g = 0;
+                                ++tok;
+                            }
+                        }
+                    }
+                } else {
+                    float* part = p.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRowsMax * (D + 2);
+#pragma unroll
+                    for (int r = 0; r < NP; ++r) {
+                        if (r < nq) {
+                            if (wt < D) __stcg(part + r * D + wt, o[r]);
+                            if (wt == 0) {
+                                __stcg(part + kRowsMax * D + r, l[r] == 0.f ? -INFINITY : mref[r]);
+                                __stcg(part + kRowsMax * (D + 1) + r, l[r]);
+                            }
                         }
                     }
                 }
             }
+            i0 = i1;
             first = false;
             ++piece;
-            bar_softmax();   // the sums were read
         }
         if (!ok) *abort_flag = 1;
     }
@@ -708,7 +824,7 @@ __global__ void __launch_bounds__(128) rows_merge_kernel(const __grid_constant__
             for (int k = 0; k < 8; ++k) {
                 const int c = c8 + k, f = first_tile(c, total, n_cta);
                 pm[k] = -INFINITY;
-                if (c <= c1 && f < first_tile(c + 1, total, n_cta)) {
+                if (c <= c1) {
                     const float* part = p.part + ((size_t)c * 2 + (T0 <= f ? 0 : 1)) * kRowsMax * (D + 2);
                     pm[k] = __ldcg(part + kRowsMax * D + r);
                     pl[k] = __ldcg(part + kRowsMax * (D + 1) + r);
@@ -758,6 +874,7 @@ cudaError_t launch_paged_rows(const PagedAttnParams& p, int n_cta, cudaStream_t 
         constexpr int D = decltype(d)::value;
         if (nq <= 8) return rows::launch<E4, D, 8>(p, n_cta, st);
         if (nq <= 16) return rows::launch<E4, D, 16>(p, n_cta, st);
+        if (nq <= 24) return rows::launch<E4, D, 24>(p, n_cta, st);
         return rows::launch<E4, D, 32>(p, n_cta, st);
     };
     using D64 = std::integral_constant<int, 64>;
