@@ -29,9 +29,10 @@
 // own S, P, O, sums and reference (a tile's chain of barriers, votes and TMEM
 // loads is ~1000 cycles long whatever the work in it; one group alone left half of
 // the stream's bandwidth unused); the first group joins the two at a pair's end.
-// Warp 8 issues S, 9 issues O, 10 looks up pages and scales and issues TMA, 11
-// loads and splits Q for the next pair.  Hand-offs are mbarriers; every wait is
-// bounded.
+// Warp 8 issues S; 9 issues O and loads and splits Q for the next pair; 10 looks up
+// pages and scales and loads K, 11 loads V (one warp for both spent 1750 cycles a
+// tile on it, more than the 1400 that its bytes take).  Hand-offs are mbarriers;
+// every wait is bounded.
 #include "masw_paged_attn.cuh"
 
 namespace masw {
@@ -65,7 +66,7 @@ struct Cfg {
     static constexpr uint32_t kOffP = kOffV + kVS * kTileB;
     static constexpr uint32_t kOffQ = kOffP + 2 * kPBuf;
     static constexpr uint32_t kOffQRaw = kOffQ + kQBufs * kQBuf;              // bf16 rows before the split
-    static constexpr uint32_t kOffSeq = kOffQRaw + (E4 ? NP * D * 2 : 0);     // pre[B + 1], kv, n, r0
+    static constexpr uint32_t kOffSeq = kOffQRaw + (E4 || kQBufs == 1 ? NP * D * 2 : 0);   // pre[B + 1], kv, n, r0
     static constexpr uint32_t kOffMeta = kOffSeq + 4 * (4 * MASW_MAX_BATCH + 4);
     static constexpr uint32_t kOffStats = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);
     // per group: row maxima and row sums of its four warps [2][4][NP], references [NP]
@@ -289,9 +290,111 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp == 9) {
-        // ---------------- O^T += V^T P^T ----------------
+        // ---------------- O^T += V^T P^T, and Q of the next piece ----------------
+        // Q in 16-byte chunks: a row is kLanes of them, a pass kPer rows; every lane
+        // splits the chunks that it copied itself.  The copies of the next piece's
+        // rows are issued at a piece's start and finished after its second tile.
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPass = NP / kPer;
+        const int e0 = (lane % kLanes) * 8, rl = lane / kLanes;
+        const uint32_t raw = sb + C::kOffQRaw + (uint32_t)lane * 16u;   // pass s: 512 bytes further
+        Walk wq = walk;
+        int q_piece = 0;
+        // K-major core matrices of 8 rows x 16 bytes, consecutive along the row
+        auto at = [&](int row, int byte) {
+            return sb + C::kOffQ + (q_piece % C::kQBufs) * C::kQBuf +
+                   (uint32_t)((row >> 3) * (C::kRB / 16) * 128 + (byte >> 4) * 128 + (row & 7) * 16 + (byte & 15));
+        };
+        auto q_free = [&]() {
+            return q_piece < C::kQBufs || all(wait(C::kQFree + q_piece % C::kQBufs, q_piece / C::kQBufs - 1));
+        };
+        auto q_issue = [&]() {
+            if (!next_piece(wq, pre, B, Hkv, s_kv, s_n, p.window)) return false;
+            // bf16: straight into the operand, once the matrix products that read it are
+            // done; with one buffer that is at the end of the piece
+            if (!E4 && C::kQBufs > 1) ok = q_free();
+            const int nq = s_n[wq.b] * G, r0 = s_r0[wq.b];
+            int tok = rl / G, g = rl - tok * G;
+#pragma unroll
+            for (int s = 0; s < kPass; ++s) {
+                const int r = s * kPer + rl;
+                const bool in = r < nq;
+                const __nv_bfloat16* src = p.q + (size_t)(r0 + (in ? tok : 0)) * p.q_stride + (size_t)(wq.h * G + (in ? g : 0)) * D + e0;
+                if (E4 || C::kQBufs == 1) {
+                    cp_async16(raw + s * 512, src, in ? 16 : 0);
+                } else {
+                    cp_async16(at(r, e0 * 2), src, in ? 16 : 0);
+                    if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
+                }
+                g += kPer;
+                while (g >= G) {
+                    g -= G;
+                    ++tok;
+                }
+            }
+            cp_async_commit();
+            return true;
+        };
+        auto q_finish = [&]() {
+            cp_async_wait<0>();
+            float inv = 1.f;
+            if constexpr (E4) {
+                float amax = 0.f;
+#pragma unroll
+                for (int s = 0; s < kPass; ++s) {
+                    const float4 v = ld_shared_v4f(raw + s * 512);
+                    float f[8];
+                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                inv = 1.f / pow2_scale(amax);
+                ok = ok && q_free();
+#pragma unroll
+                for (int s = 0; s < kPass; ++s) {
+                    const int r = s * kPer + rl;
+                    const float4 v = ld_shared_v4f(raw + s * 512);
+                    float f[8];
+                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
+                    uint32_t w1[4], w2[4];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float a = f[e] * inv, b = f[e + 1] * inv;
+                        const uint32_t q1 = e4m3x2(a, b);
+                        float a1, b1;
+                        f16x2_to_f32(e4m3x2_to_f16x2(q1), a1, b1);
+                        w1[e / 2] = q1;
+                        w2[e / 2] = e4m3x2((a - a1) * 16.f, (b - b1) * 16.f);
+                    }
+                    st_shared_v2(at(r, e0), w1[0] | (w1[1] << 16), w1[2] | (w1[3] << 16));
+                    st_shared_v2(at(NP + r, e0), w2[0] | (w2[1] << 16), w2[2] | (w2[3] << 16));
+                }
+            } else if constexpr (C::kQBufs == 1) {
+                ok = ok && q_free();
+#pragma unroll
+                for (int s = 0; s < kPass; ++s) {
+                    const int r = s * kPer + rl;
+                    const float4 v = ld_shared_v4f(raw + s * 512);
+                    const uint4 x = *reinterpret_cast<const uint4*>(&v);
+                    st_shared_v4(at(r, e0 * 2), x.x, x.y, x.z, x.w);
+                    if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
+                }
+            }
+            if (!ok) return;
+            const int qb = q_piece % C::kQBufs;
+            if (lane == 0) qscale[qb] = p.scale_log2 / inv;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_at(C::kQFull + qb));
+            ++q_piece;
+        };
+        // one operand buffer: it is free only when the piece's own products are done
+        constexpr bool kLate = C::kQBufs == 1;
+        if (q_issue()) q_finish();
         int i = 0;
         while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
+            bool pending = q_issue();
             for (int j = 0; ok && j < walk.nt; ++j, ++i) {
                 const int st = i % C::kVS, pb = i & 1;
                 ok = all(wait(C::kPFull + pb, i / 2)) && all(wait(C::kVFull + st, i / C::kVS));
@@ -314,63 +417,68 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     umma_commit(bar_at(C::kVFree + st));
                 }
                 __syncwarp();
+                if (pending && j + 1 == (kLate ? walk.nt : imin(2, walk.nt))) {
+                    q_finish();
+                    pending = false;
+                }
             }
         }
+        // nothing may arrive on a barrier after the CTA ended
         if (ok && i > 0) ok = all(wait(C::kVFree + (i - 1) % C::kVS, (i - 1) / C::kVS));
         if (!ok) {
             *abort_flag = 1;
+            cp_async_wait<0>();
             if (elect_one()) umma_commit(bar_at(C::kDone + 1));
             __syncwarp();
             mbar_wait(bars + C::kDone + 1, 0, nullptr);
         }
         __syncwarp();
-    } else if (warp == 10) {
-        // ---------------- page ids, scales, TMA ----------------
+    } else {
+        // ---------------- page ids and TMA: warp 10 K and the scales, warp 11 V ----------------
         // A lane holds the page of one box (at most 128 rows of a page); a batch
-        // is up to 32 boxes of a piece.  The next batch's page ids are loaded
-        // while the current one is issued, and its scales once they are there.
+        // is up to 32 boxes of a piece.  Page ids are loaded two batches ahead, scales
+        // one.
+        const bool is_v = warp == 11;
+        const int stages = is_v ? C::kVS : C::kKS, full = is_v ? C::kVFull : C::kKFull, freed = is_v ? C::kVFree : C::kKFree;
+        const uint32_t ring = sb + (is_v ? C::kOffV : C::kOffK);
+        const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
+        const bool scales = E4 && !is_v;
         const int box = imin(c.P, kTile), bpt = kTile / box, bt = 32 / bpt;   // boxes a tile, tiles a batch
-        Walk w = walk;
         int left = 0, at = 0;            // tiles of the piece not yet in a batch, and the first of them
-        struct Batch { int h, tile, nt, pid, lo, hi; bool in; float ks, lvs, ivs; };   // boxes [lo, hi) hold visible keys
+        struct Batch { int h, tile, nt, pid, lo, hi; bool in; float ks, vs; };   // boxes [lo, hi) hold visible keys
         auto next_batch = [&](Batch& x) {
             x.nt = 0;
             x.in = false;
             if (left == 0) {
-                if (!next_piece(w, pre, B, Hkv, s_kv, s_n, p.window)) return;
-                left = w.nt;
-                at = w.tile;
+                if (!next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) return;
+                left = walk.nt;
+                at = walk.tile;
             }
-            x.h = w.h;
+            x.h = walk.h;
             x.tile = at;
             x.nt = imin(left, bt);
             at += x.nt;
             left -= x.nt;
-            const TileRange r = tile_range(s_n[w.b], s_kv[w.b], p.window);
+            const TileRange r = tile_range(s_n[walk.b], s_kv[walk.b], p.window);
             const int key0 = x.tile * kTile;
             x.lo = imax(0, r.lo / c.P * c.P - key0) / box;   // pages wholly before the first visible key are left out
             x.hi = imin(x.nt * bpt, (r.hi - key0 + box - 1) / box);
             x.in = lane >= x.lo && lane < x.hi;
-            x.pid = x.in ? __ldg(c.table + (size_t)w.b * c.table_stride + (key0 + lane * box) / c.P) : 0;
+            x.pid = x.in ? __ldg(c.table + (size_t)walk.b * c.table_stride + (key0 + lane * box) / c.P) : 0;
         };
         auto check_and_scale = [&](Batch& x) {
             if (x.in && (x.pid < 0 || x.pid >= c.n_pages)) {
                 atomicExch(err, MASW_EINVAL);
                 x.pid = 0;
             }
-            if (E4) {
-                float vs = 1.f;
-                x.ks = 1.f;
-                if (x.in) {
-                    x.ks = __ldg(c.k_scale + (size_t)x.pid * Hkv + x.h);
-                    vs = __ldg(c.v_scale + (size_t)x.pid * Hkv + x.h);
-                }
-                x.lvs = vs == 1.f ? 0.f : __log2f(vs);
-                x.ivs = __frcp_rn(vs);
+            x.ks = x.vs = 1.f;
+            if (scales && x.in) {
+                x.ks = __ldg(c.k_scale + (size_t)x.pid * Hkv + x.h);
+                x.vs = __ldg(c.v_scale + (size_t)x.pid * Hkv + x.h);
             }
         };
         Batch cur, nxt;
-        int i = 0;
+        int i = 0, st = 0, turn = 0;     // tile, its stage, and how often the ring went round
         next_batch(cur);
         next_batch(nxt);
         check_and_scale(cur);
@@ -378,136 +486,45 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             check_and_scale(nxt);
             Batch nn;
             next_batch(nn);
-            for (int j = 0; ok && j < cur.nt; ++j, ++i) {
-                const int ks = i % C::kKS, vs = i % C::kVS;
+            const float lvs = cur.vs == 1.f ? 0.f : __log2f(cur.vs), ivs = __frcp_rn(cur.vs);
+            for (int j = 0; j < cur.nt; ++j, ++i) {
                 const int b0 = imax(cur.lo, j * bpt), b1 = imin(cur.hi, (j + 1) * bpt);   // the tile's boxes
-                const uint32_t bytes = (uint32_t)(imax(0, b1 - b0) * box * C::kRB);
-                auto load = [&](const CUtensorMap* map, uint32_t tile, int bar) {
-                    // the whole warp walks the boxes, one lane issues
-                    for (int q = b0; q < b1; ++q) {
-                        const int pid = __shfl_sync(0xffffffffu, cur.pid, q);
-                        const int row = (cur.tile * kTile + q * box) & (c.P - 1);
-                        const uint32_t dst = tile + (uint32_t)((q - j * bpt) * box * C::kPB);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int pn = 0; pn < C::kPanels; ++pn)
-                                tma_load_4d(dst + pn * C::kPanel, map, pn * C::kPB / C::kES, row, cur.h, pid, bar_at(bar));
-                        }
-                    }
-                    __syncwarp();
-                };
-                if (i >= C::kKS) ok = all(wait(C::kKFree + ks, i / C::kKS - 1));
+                if (turn > 0) ok = all(wait(freed + st, turn - 1));
                 if (!ok) break;
-                if (E4) {
-                    if (lane / bpt == j) meta[(i % kMeta) * 8 + lane % bpt] = make_float4(cur.ks, cur.lvs, cur.ivs, 0.f);
+                if (scales) {
+                    if (lane / bpt == j) meta[(i % kMeta) * 8 + lane % bpt] = make_float4(cur.ks, lvs, ivs, 0.f);
                     __syncwarp();
                 }
                 if (elect_one()) {
-                    if (E4) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
-                    mbar_expect_tx(bars + C::kKFull + ks, bytes);
+                    if (scales) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
+                    mbar_expect_tx(bars + full + st, (uint32_t)(imax(0, b1 - b0) * box * C::kRB));
                 }
                 __syncwarp();
-                load(&p.tm_k, sb + C::kOffK + ks * C::kTileB, C::kKFull + ks);
-                if (i >= C::kVS) ok = all(wait(C::kVFree + vs, i / C::kVS - 1));
-                if (!ok) {   // the K tile was issued, its V tile was not
-                    mbar_wait(bars + C::kKFull + ks, (uint32_t)(i / C::kKS) & 1u, nullptr);
-                    break;
+                // the whole warp walks the boxes, one lane issues
+                for (int q = b0; q < b1; ++q) {
+                    const int pid = __shfl_sync(0xffffffffu, cur.pid, q);
+                    const int row = (cur.tile * kTile + q * box) & (c.P - 1);
+                    const uint32_t dst = ring + st * C::kTileB + (uint32_t)((q - j * bpt) * box * C::kPB);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int pn = 0; pn < C::kPanels; ++pn)
+                            tma_load_4d(dst + pn * C::kPanel, map, pn * C::kPB / C::kES, row, cur.h, pid, bar_at(full + st));
+                    }
                 }
-                if (elect_one()) mbar_expect_tx(bars + C::kVFull + vs, bytes);
                 __syncwarp();
-                load(&p.tm_v, sb + C::kOffV + vs * C::kTileB, C::kVFull + vs);
+                if (++st == stages) {
+                    st = 0;
+                    ++turn;
+                }
             }
             cur = nxt;
             nxt = nn;
         }
         // after a wait gave up, and at the end: no copy may be in flight when the CTA ends
         if (!ok) *abort_flag = 1;
-        for (int k = imax(0, i - C::kKS); k < i; ++k)
-            mbar_wait(bars + C::kKFull + k % C::kKS, (uint32_t)(k / C::kKS) & 1u, nullptr);
-        for (int k = imax(0, i - C::kVS); k < i; ++k)
-            mbar_wait(bars + C::kVFull + k % C::kVS, (uint32_t)(k / C::kVS) & 1u, nullptr);
+        for (int k = imax(0, i - stages); k < i; ++k)
+            mbar_wait(bars + full + k % stages, (uint32_t)(k / stages) & 1u, nullptr);
         __syncwarp();
-    } else if (warp == 11) {
-        // ---------------- Q of the next pair ----------------
-        // 16-byte chunks: a row is kLanes of them, a pass kPer rows; every lane
-        // splits the chunks that it copied itself
-        constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPass = NP / kPer;
-        const int e0 = (lane % kLanes) * 8, rl = lane / kLanes;
-        int piece = 0;
-        while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
-            const int nq = s_n[walk.b] * G, r0 = s_r0[walk.b];
-            const int qb = piece % C::kQBufs;
-            const uint32_t qbase = sb + C::kOffQ + qb * C::kQBuf;
-            // K-major core matrices of 8 rows x 16 bytes, consecutive along the row
-            auto at = [&](int row, int byte) {
-                return qbase + (uint32_t)((row >> 3) * (C::kRB / 16) * 128 + (byte >> 4) * 128 + (row & 7) * 16 + (byte & 15));
-            };
-            const uint32_t raw = sb + C::kOffQRaw + (uint32_t)lane * 16u;   // pass s: 512 bytes further
-            if (!E4 && piece >= C::kQBufs) ok = all(wait(C::kQFree + qb, piece / C::kQBufs - 1));
-            if (!ok) break;
-            int tok = rl / G, g = rl - tok * G;
-#pragma unroll
-            for (int s = 0; s < kPass; ++s) {
-                const int r = s * kPer + rl;
-                const bool in = r < nq;
-                const __nv_bfloat16* src = p.q + (size_t)(r0 + (in ? tok : 0)) * p.q_stride + (size_t)(walk.h * G + (in ? g : 0)) * D + e0;
-                if (E4) {
-                    cp_async16(raw + s * 512, src, in ? 16 : 0);
-                } else {
-                    cp_async16(at(r, e0 * 2), src, in ? 16 : 0);
-                    if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
-                }
-                g += kPer;
-                while (g >= G) {
-                    g -= G;
-                    ++tok;
-                }
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            float inv = 1.f;
-            if constexpr (E4) {
-                float amax = 0.f;
-#pragma unroll
-                for (int s = 0; s < kPass; ++s) {
-                    const float4 v = ld_shared_v4f(raw + s * 512);
-                    float f[8];
-                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
-                }
-#pragma unroll
-                for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                inv = 1.f / pow2_scale(amax);
-                if (piece >= C::kQBufs) ok = all(wait(C::kQFree + qb, piece / C::kQBufs - 1));
-                if (!ok) break;
-#pragma unroll
-                for (int s = 0; s < kPass; ++s) {
-                    const int r = s * kPer + rl;
-                    const float4 v = ld_shared_v4f(raw + s * 512);
-                    float f[8];
-                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
-                    uint32_t w1[4], w2[4];
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float a = f[e] * inv, b = f[e + 1] * inv;
-                        const uint32_t q1 = e4m3x2(a, b);
-                        float a1, b1;
-                        f16x2_to_f32(e4m3x2_to_f16x2(q1), a1, b1);
-                        w1[e / 2] = q1;
-                        w2[e / 2] = e4m3x2((a - a1) * 16.f, (b - b1) * 16.f);
-                    }
-                    st_shared_v2(at(r, e0), w1[0] | (w1[1] << 16), w1[2] | (w1[3] << 16));
-                    st_shared_v2(at(NP + r, e0), w2[0] | (w2[1] << 16), w2[2] | (w2[3] << 16));
-                }
-            }
-            if (lane == 0) qscale[qb] = p.scale_log2 / inv;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_at(C::kQFull + qb));
-            ++piece;
-        }
-        if (!ok) *abort_flag = 1;
     }
     } else {
         take_registers<NP>();
@@ -803,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     }
 }
 
-// Joins the pieces of the pairs that were cut.  CTA (pair, 4 rows); thread d
-// owns output element d.
+// Joins the pieces of the pairs that were cut.  CTA (pair, row); thread d owns
+// output element d.
 template <int D>
 __global__ void __launch_bounds__(128) rows_merge_kernel(const __grid_constant__ PagedAttnParams p, int n_cta) {
     __shared__ int pre[MASW_MAX_BATCH + 1], s_kv[MASW_MAX_BATCH], s_n[MASW_MAX_BATCH], s_r0[MASW_MAX_BATCH];
@@ -816,35 +833,41 @@ __global__ void __launch_bounds__(128) rows_merge_kernel(const __grid_constant__
     if (per == 0) return;
     const int c0 = tile_owner(T0, total, n_cta), c1 = tile_owner(T1 - 1, total, n_cta);
     if (c0 == c1) return;
-    for (int r = blockIdx.y * 4; r < imin(nq, (int)blockIdx.y * 4 + 4); ++r) {
-        float M = -INFINITY, l = 0.f, o = 0.f;
-        for (int c8 = c0; c8 <= c1; c8 += 8) {
-            float pm[8], pl[8], po[8];
+    const int r = blockIdx.y;
+    if (r >= nq) return;
+    float M = -INFINITY, l = 0.f, o = 0.f;
+    for (int c8 = c0; c8 <= c1; c8 += 10) {
+        float pm[10], pl[10], po[10];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = c8 + k, f = first_tile(c, total, n_cta);
-                pm[k] = -INFINITY;
-                if (c <= c1) {
-                    const float* part = p.part + ((size_t)c * 2 + (T0 <= f ? 0 : 1)) * kRowsMax * (D + 2);
-                    pm[k] = __ldcg(part + kRowsMax * D + r);
-                    pl[k] = __ldcg(part + kRowsMax * (D + 1) + r);
-                    po[k] = __ldcg(part + r * D + tid % D);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (pm[k] == -INFINITY) continue;
-                const float nm = fmaxf(M, pm[k]);
-                const float w0 = exp2f(M - nm), w1 = exp2f(pm[k] - nm);
-                l = l * w0 + pl[k] * w1;
-                o = o * w0 + po[k] * w1;
-                M = nm;
+        for (int k = 0; k < 10; ++k) {
+            const int c = c8 + k;
+            pm[k] = -INFINITY;
+            pl[k] = po[k] = 0.f;
+            if (c <= c1) {
+                const float* part = p.part + ((size_t)c * 2 + (T0 <= first_tile(c, total, n_cta) ? 0 : 1)) * kRowsMax * (D + 2);
+                pm[k] = __ldcg(part + kRowsMax * D + r);
+                pl[k] = __ldcg(part + kRowsMax * (D + 1) + r);
+                po[k] = __ldcg(part + r * D + tid % D);
             }
         }
-        const size_t row = (size_t)(s_r0[b] + r / G) * p.Hq + h * G + r % G;
-        if (tid < D) store_out(p, row * D + tid, l == 0.f ? 0.f : o / l);
-        if (tid == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+        float m8 = M;
+#pragma unroll
+        for (int k = 0; k < 10; ++k) m8 = fmaxf(m8, pm[k]);
+        if (m8 == -INFINITY) continue;
+        const float w = exp2f(M - m8);
+        l *= w;
+        o *= w;
+        M = m8;
+#pragma unroll
+        for (int k = 0; k < 10; ++k) {
+            const float wk = exp2f(pm[k] - M);
+            l = fmaf(pl[k], wk, l);
+            o = pm[k] == -INFINITY ? o : fmaf(po[k], wk, o);
+        }
     }
+    const size_t row = (size_t)(s_r0[b] + r / G) * p.Hq + h * G + r % G;
+    if (tid < D) store_out(p, row * D + tid, l == 0.f ? 0.f : o / l);
+    if (tid == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
 }
 
 template <bool E4, int D, int NP>
@@ -862,7 +885,7 @@ cudaError_t launch(const PagedAttnParams& p, int n_cta, cudaStream_t st) {
     e = masw_launch(rows_kernel<E4, D, NP>, dim3(n_cta), dim3(kThreads), C::kSmem, st, 1, p);
     if (e != cudaSuccess) return e;
     const int nq = p.max_rows * p.G;
-    return masw_launch(rows_merge_kernel<D>, dim3(p.c.B * p.c.Hkv, (nq + 3) / 4), dim3(128), 0, st, 1, p, n_cta);
+    return masw_launch(rows_merge_kernel<D>, dim3(p.c.B * p.c.Hkv, nq), dim3(128), 0, st, 1, p, n_cta);
 }
 
 }  // namespace rows
