@@ -123,6 +123,7 @@ static int paged_attn_sizes(const PagedView& c, const char* who, int rows, int m
     if (ragged && max_rows < 0) return fail("max_rows must not be negative");
     if (n_q_heads < c.Hkv || n_q_heads % c.Hkv || n_q_heads / c.Hkv > 128)
         return fail("n_q_heads must be a multiple of n_kv_heads, at most 128 per kv head");
+    if ((long long)rows * n_q_heads > 0x7fffffffll) return fail("rows * n_q_heads must be below 2^31");
     *mr = ragged ? std::min(max_rows, rows) : rows / c.B;
     if ((long long)c.B * c.Hkv * (c.cap / kTile + 2) > 0x7fffffffll) return fail("batch * heads * table too large");
     return MASW_OK;

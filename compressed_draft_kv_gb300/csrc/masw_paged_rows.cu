@@ -69,9 +69,12 @@ struct Cfg {
     static constexpr uint32_t kOffSeq = kOffQRaw + (E4 || kQBufs == 1 ? NP * D * 2 : 0);   // pre[B + 1], kv, n, r0
     static constexpr uint32_t kOffMeta = kOffSeq + 4 * (4 * MASW_MAX_BATCH + 4);
     static constexpr uint32_t kOffStats = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);
-    // per group: row maxima and row sums of its four warps [2][4][NP], references [NP]
-    static constexpr int kStats = 9 * NP;
-    static constexpr uint32_t kOffQs = kOffStats + 2 * kStats * 4;             // scale of Q per buffer
+    // floats of a group: row maxima [4][NP] of its warps, references [NP], factors
+    // [NP], and published at a piece's end: row sums [4][NP] and references [NP];
+    // then the joined weights of both groups [2][NP] and the rows' places [NP]
+    static constexpr int kRef = 4 * NP, kFac = 5 * NP, kSums = 6 * NP, kOut = 10 * NP, kStats = 11 * NP;
+    static constexpr int kFin = 2 * kStats, kRow = kFin + 2 * NP, kStatFloats = kRow + NP;
+    static constexpr uint32_t kOffQs = kOffStats + kStatFloats * 4;            // scale of Q per buffer, unset rows per group
     static constexpr uint32_t kOffBar = kOffQs + 16;
     // barriers
     static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kMetaBar = kVFree + kVS;
@@ -161,6 +164,12 @@ __device__ __forceinline__ void take_registers() {
 template <int NP>
 __device__ __forceinline__ void give_registers() {
     if constexpr (NP > 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+}
+
+__device__ __forceinline__ float warp_max(float x) {   // in every lane; NaN does not count
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
@@ -292,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     } else if (warp == 9) {
         // ---------------- O^T += V^T P^T, and Q of the next piece ----------------
         // Q in 16-byte chunks: a row is kLanes of them, a pass kPer rows; every lane
-        // splits the chunks that it copied itself.  The copies of the next piece's
+        // splits the chunks that it copied itself.  Loops stay rolled, here and wherever
+        // code runs once a piece: fetching instructions for the first time costs more
+        // than running them.  The copies of the next piece's
         // rows are issued at a piece's start and finished after its second tile.
         constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPass = NP / kPer;
         const int e0 = (lane % kLanes) * 8, rl = lane / kLanes;
@@ -314,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             if (!E4 && C::kQBufs > 1) ok = q_free();
             const int nq = s_n[wq.b] * G, r0 = s_r0[wq.b];
             int tok = rl / G, g = rl - tok * G;
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < kPass; ++s) {
                 const int r = s * kPer + rl;
                 const bool in = r < nq;
@@ -339,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             float inv = 1.f;
             if constexpr (E4) {
                 float amax = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int s = 0; s < kPass; ++s) {
                     const float4 v = ld_shared_v4f(raw + s * 512);
                     float f[8];
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 inv = 1.f / pow2_scale(amax);
                 ok = ok && q_free();
-#pragma unroll
+#pragma unroll 1
                 for (int s = 0; s < kPass; ++s) {
                     const int r = s * kPer + rl;
                     const float4 v = ld_shared_v4f(raw + s * 512);
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 }
             } else if constexpr (C::kQBufs == 1) {
                 ok = ok && q_free();
-#pragma unroll
+#pragma unroll 1
                 for (int s = 0; s < kPass; ++s) {
                     const int r = s * kPer + rl;
                     const float4 v = ld_shared_v4f(raw + s * 512);
@@ -536,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         const uint32_t t_s = tmem + group * C::kSN + lane_off;
         const uint32_t t_o = tmem + C::kColO + lane_off;             // group 0's; group 1's kPN columns further
         const uint32_t t_own = t_o + group * C::kPN;
-        float* red = stats + group * C::kStats;                     // [4][NP] row maxima of the group's warps
-        float* sums = red + 4 * NP;                                  // [4][NP] row sums
-        float* ref = sums + 4 * NP;                                  // [NP] references
+        float* own = stats + group * C::kStats;
+        const uint32_t own_a = smem_u32(own);
+        uint32_t* unset_word = reinterpret_cast<uint32_t*>(qscale) + 2 + group;
         int i0 = 0, piece = 0;
         bool first = true;
         while (next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
@@ -550,9 +561,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             // rows without a reference yet, because they have seen no key (the same in
             // every thread of the group)
             uint32_t unset = nq == 32 ? 0xffffffffu : (1u << nq) - 1u;
-            float mref[NP], l[NP];
+            float l[NP];
 #pragma unroll
-            for (int r = 0; r < NP; ++r) mref[r] = l[r] = 0.f;
+            for (int r = 0; r < NP; ++r) l[r] = 0.f;
+            if (wt < NP) own[C::kRef + wt] = 0.f;
+            bar_group(group);
             ok &= wait(C::kQFull + qb, piece / C::kQBufs);
             const float qs = qscale[qb];
             __syncwarp();
@@ -614,9 +627,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                         tmem_ld_cols<E4 ? 2 * NP : NP>(t_s, sv);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int r = 0; r < NP; ++r) {
-                            const float x = E4 ? fmaf(__uint_as_float(sv[NP + r]), 0.0625f, __uint_as_float(sv[r])) : __uint_as_float(sv[r]);
-                            a[r] = fmaf(x, ks, lvs - mref[r]);
+                        for (int r = 0; r < NP; r += 4) {
+                            const float4 m = ld_shared_v4f(own_a + (C::kRef + r) * 4);
+                            const float mr[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float x = E4 ? fmaf(__uint_as_float(sv[NP + r + e]), 0.0625f, __uint_as_float(sv[r + e]))
+                                                   : __uint_as_float(sv[r + e]);
+                                a[r + e] = fmaf(x, ks, lvs - mr[e]);
+                            }
                         }
                     }
                     if (masked) {
@@ -634,45 +653,52 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     if (!bar_or(group, move)) break;
 #pragma unroll
                     for (int r = 0; r < NP; ++r) {
-                        float s = a[r];
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-                        if (lane == 0) red[gw * NP + r] = s;
+                        const float s = warp_max(a[r]);
+                        if (lane == 0) own[gw * NP + r] = s;
                     }
                     bar_group(group);
-                    if (j > 1 && !p_free) {
+                    if (gw == 0) {
+                        float top = -INFINITY;
+                        if (lane < NP) {
+                            top = fmaxf(fmaxf(own[lane], own[NP + lane]), fmaxf(own[2 * NP + lane], own[3 * NP + lane]));
+                            const bool fresh = (unset >> lane) & 1u;
+                            const float up = fresh ? (top > -3e38f ? top - C::kHead : 0.f) : fmaxf(0.f, top - C::kHead);
+                            own[C::kRef + lane] += up;
+                            own[C::kFac + lane] = fresh ? 1.f : ex2_approx(-up);   // what the sums and O shrink by
+                        }
+                        const uint32_t seen_now = __ballot_sync(0xffffffffu, top > -3e38f);
+                        if (lane == 0) *unset_word = unset & ~seen_now;
+                    }
+                    bar_group(group);
+                    unset = *reinterpret_cast<volatile uint32_t*>(unset_word);
+#pragma unroll
+                    for (int r = 0; r < NP; r += 4) {
+                        const float4 f = ld_shared_v4f(own_a + (C::kFac + r) * 4);
+                        l[r] *= f.x;
+                        l[r + 1] *= f.y;
+                        l[r + 2] *= f.z;
+                        l[r + 3] *= f.w;
+                    }
+                    if (j > 1) {
                         // O holds the group's earlier tiles of the piece once the last product is done
-                        ok &= wait(C::kPFree + group, turn - 1);
+                        if (!p_free) ok &= wait(C::kPFree + group, turn - 1);
+                        p_free = true;
                         __syncwarp();
                         tc_fence_after();
-                        p_free = true;
-                    }
-                    uint32_t now_set = 0u;
-#pragma unroll
-                    for (int r = 0; r < NP; ++r) {
-                        const float top = fmaxf(fmaxf(red[r], red[NP + r]), fmaxf(red[2 * NP + r], red[3 * NP + r]));
-                        const bool fresh = (unset >> r) & 1u;
-                        const float up = fresh ? (top > -3e38f ? top - C::kHead : 0.f) : fmaxf(0.f, top - C::kHead);
-                        mref[r] += up;
-                        a[r] = fresh ? 1.f : ex2_approx(-up);   // what the sums and O shrink by
-                        l[r] *= a[r];
-                        if (top > -3e38f) now_set |= 1u << r;
-                    }
-                    unset &= ~now_set;
-                    if (j > 1) {
-#pragma unroll
-                        for (int q = 0; q < C::kPN / 8; ++q) {
+#pragma unroll 1
+                        for (int q = 0; q < C::kPN; q += 8) {
                             uint32_t ov[8];
-                            tmem_ld8(t_own + q * 8, ov);
+                            tmem_ld8(t_own + q, ov);
                             tmem_wait_ld();
+                            const uint32_t fa = own_a + (C::kFac + q % NP) * 4;
+                            const float4 f0 = ld_shared_v4f(fa), f1 = ld_shared_v4f(fa + 16);
+                            const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * a[(q * 8 + e) % NP]);
-                            tmem_st8(t_own + q * 8, ov);
+                            for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f[e]);
+                            tmem_st8(t_own + q, ov);
                         }
                         tmem_wait_st();
                     }
-                    bar_group(group);   // the maxima were read
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -715,96 +741,96 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_at(C::kPFull + group));
             }
-            // the piece's sums over the group's keys
-#pragma unroll
-            for (int r = 0; r < NP; ++r) {
-#pragma unroll
-                for (int o = 16; o; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-            }
+            // the piece's sums over the group's keys: eight rows at a time, a butterfly
+            // that halves the rows with every step; lane 4 k ends with row k's sum
             if (!o_free) ok &= wait(C::kOFree, piece - 1);
 #pragma unroll
-            for (int r = 0; r < NP; ++r) {
-                if (lane == 0) sums[gw * NP + r] = l[r];
-                if (wt == 0) ref[r] = (unset >> r) & 1u ? -1e30f : mref[r];
+            for (int q = 0; q < NP; q += 8) {
+#pragma unroll
+                for (int h = 4; h >= 1; h >>= 1) {
+                    const bool up = lane & (4 * h);
+#pragma unroll
+                    for (int e = 0; e < h; ++e) {
+                        const float keep = up ? l[q + h + e] : l[q + e], give = up ? l[q + e] : l[q + h + e];
+                        l[q + e] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
+                    }
+                }
+                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
+                l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
+                if ((lane & 3) == 0) own[C::kSums + gw * NP + q + (lane >> 2)] = l[q];
             }
+            if (wt < NP) own[C::kOut + wt] = (unset >> wt) & 1u ? -1e30f : own[C::kRef + wt];
             const int i1 = i0 + walk.nt;
             if (group == 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_at(C::kStat));
             } else {
-                // join the two groups' sums and O (group g's last tile before i1: the
-                // one or two in the piece)
+                // join the two groups: thread r the sums of row r, then thread d the
+                // outputs of element d
+                const bool had0 = walk.nt > 1 || !(i0 & 1), had1 = walk.nt > 1 || (i0 & 1);
+                float* part = p.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRowsMax * (D + 2);
                 bar_group(group);
                 ok &= wait(C::kStat, piece);
-                const float* other = stats + C::kStats;
-                const bool had0 = walk.nt > 1 || !(i0 & 1), had1 = walk.nt > 1 || (i0 & 1);
+                if (wt < NP) {
+                    const int r = wt;
+                    const float* s0 = stats + r;
+                    const float* s1 = s0 + C::kStats;
+                    const float m0 = s0[C::kOut], m1 = s1[C::kOut], m = fmaxf(m0, m1);
+                    float w0 = ex2_approx(m0 - m), w1 = ex2_approx(m1 - m);
+                    const float sum = (s0[C::kSums] + s0[C::kSums + NP] + s0[C::kSums + 2 * NP] + s0[C::kSums + 3 * NP]) * w0 +
+                                      (s1[C::kSums] + s1[C::kSums + NP] + s1[C::kSums + 2 * NP] + s1[C::kSums + 3 * NP]) * w1;
+                    int place = r;
+                    if (walk.whole) {
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        w0 *= inv;
+                        w1 *= inv;
+                        place = (s_r0[b] + r / G) * p.Hq + walk.h * G + r % G;
+                        if (r < nq && p.lse) p.lse[place] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.6931471805599453f;
+                    } else if (r < nq) {
+                        __stcg(part + kRowsMax * D + r, sum == 0.f ? -INFINITY : m);
+                        __stcg(part + kRowsMax * (D + 1) + r, sum);
+                    }
+                    stats[C::kFin + r] = w0;
+                    stats[C::kFin + NP + r] = w1;
+                    reinterpret_cast<int*>(stats)[C::kRow + r] = place;
+                }
                 if (had0) ok &= wait(C::kPFree, (i1 - 1) >> 1);
                 if (had1) ok &= wait(C::kPFree + 1, (i1 - 2) >> 1);
-                __syncwarp();
+                bar_group(group);
                 tc_fence_after();
-                float o[NP];
-                {
-                    float w0[NP], w1[NP];
+                const bool f32 = p.o_f32 || !walk.whole;
+                float* fdst = walk.whole ? reinterpret_cast<float*>(p.o) : part;
+#pragma unroll 1
+                for (int q = 0; q < nq; q += 8) {
+                    float o[8];
 #pragma unroll
-                    for (int r = 0; r < NP; ++r) {
-                        const float m0 = ref[r], m1 = other[8 * NP + r], m = fmaxf(m0, m1);
-                        const float l0 = sums[r] + sums[NP + r] + sums[2 * NP + r] + sums[3 * NP + r];
-                        const float l1 = other[4 * NP + r] + other[5 * NP + r] + other[6 * NP + r] + other[7 * NP + r];
-                        w0[r] = ex2_approx(m0 - m);
-                        w1[r] = ex2_approx(m1 - m);
-                        l[r] = l0 * w0[r] + l1 * w1[r];
-                        mref[r] = m;
-                        o[r] = 0.f;
+                    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (!(g ? had1 : had0)) continue;
+                        uint32_t u[8], v[8];
+                        tmem_ld8(t_o + g * C::kPN + q, u);
+                        tmem_ld8(t_o + g * C::kPN + NP + q, v);
+                        const uint32_t wa = smem_u32(stats + C::kFin + g * NP + q);
+                        const float4 w0 = ld_shared_v4f(wa), w1 = ld_shared_v4f(wa + 16);
+                        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = fmaf(fmaf(__uint_as_float(v[e]), E4 ? 0.0625f : 1.f, __uint_as_float(u[e])), w[e], o[e]);
                     }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float f = E4 && k == 1 ? 0.0625f : 1.f;
-#pragma unroll
-                        for (int q = 0; q < NP / 8; ++q) {
-                            uint32_t u[8], v[8];
-                            tmem_ld8(t_o + k * NP + q * 8, u);
-                            tmem_ld8(t_o + C::kPN + k * NP + q * 8, v);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int r = q * 8 + e;
-                                if (had0) o[r] = fmaf(__uint_as_float(u[e]), f * w0[r], o[r]);
-                                if (had1) o[r] = fmaf(__uint_as_float(v[e]), f * w1[r], o[r]);
-                            }
+                    for (int e = 0; e < 8; ++e) {
+                        if (q + e < nq && wt < D) {
+                            const size_t at = (size_t)reinterpret_cast<const int*>(stats)[C::kRow + q + e] * D + wt;
+                            if (f32) __stcg(fdst + at, o[e]);
+                            else reinterpret_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(o[e]);
                         }
                     }
                 }
                 tc_fence_before();
-                bar_group(group);   // the sums were read
+                bar_group(group);   // the joined weights were read
                 if (lane == 0) mbar_arrive(bar_at(C::kOFree));
-                if (walk.whole) {
-                    int tok = s_r0[b], g = 0;
-#pragma unroll
-                    for (int r = 0; r < NP; ++r) {
-                        if (r < nq) {
-                            const size_t row = (size_t)tok * p.Hq + walk.h * G + g;
-                            if (wt < D) store_out(p, row * D + wt, l[r] == 0.f ? 0.f : o[r] / l[r]);
-                            if (wt == 0 && p.lse)
-                                p.lse[row] = l[r] == 0.f ? -INFINITY : (mref[r] + __log2f(l[r])) * 0.6931471805599453f;
-                            if (++g == G) {
-                                g = 0;
-                                ++tok;
-                            }
-                        }
-                    }
-                } else {
-                    float* part = p.part + ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRowsMax * (D + 2);
-#pragma unroll
-                    for (int r = 0; r < NP; ++r) {
-                        if (r < nq) {
-                            if (wt < D) __stcg(part + r * D + wt, o[r]);
-                            if (wt == 0) {
-                                __stcg(part + kRowsMax * D + r, l[r] == 0.f ? -INFINITY : mref[r]);
-                                __stcg(part + kRowsMax * (D + 1) + r, l[r]);
-                            }
-                        }
-                    }
-                }
             }
             i0 = i1;
             first = false;
