@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmasw.so")
 SOURCES = ["masw_pool.cu", "masw_decode.cu", "masw_decode_mma.cu", "masw_verify.cu", "masw_accept.cu", "masw_prefill.cu",
-           "masw_paged.cu", "masw_paged_attn.cu", "masw_paged_rows.cu"]
+           "masw_paged.cu", "masw_paged_attn.cu", "masw_paged_rows.cu", "masw_paged_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,10 +1,10 @@
 // Causal attention of ragged query blocks over a paged cache in bf16 or e4m3
 // ([EN] §2.3 Eq. 2, §3.3 Algorithm 2).
 //
-// One CTA per (16 query rows of a kv head, sequence): a row is (query token,
-// query head of the group).  Keys pass through shared memory in fp32, 32 at a
-// time; a warp owns two rows, its lanes hold a score each and four output
-// elements each, with the running maximum and sum of the softmax.
+// Two kernels, by the number of query rows (query token x query head of the
+// group) of a (sequence, kv head) pair: up to 32 go to the few-rows kernel
+// (masw_paged_rows.cu: keys as the matrix rows, bound by reading the cache), more
+// to the many-rows kernel (masw_paged_tile.cu: query rows as the matrix rows).
 #include "masw_paged_attn.cuh"
 
 #include <algorithm>
@@ -12,104 +12,15 @@
 
 namespace masw {
 
-constexpr int kSimpleRows = 16, kSimpleKeys = 32;
-
-__global__ void __launch_bounds__(256) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
-    extern __shared__ float fs[];
-    const PagedView& c = p.c;
-    const int D = c.D, LD = D + 1;
-    float* qs = fs;                              // [16][D]
-    float* ks = qs + kSimpleRows * D;            // [32][D + 1]
-    float* vs = ks + kSimpleKeys * LD;           // [32][D + 1]
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_wait();
-    pdl_trigger();
-    const int b = blockIdx.z, h = blockIdx.y, G = p.G;
-    const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
-    const bool bad = !s.ok || s.n > p.max_rows;
-    if (bad && tid == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
-    if (bad) return;
-    const int n0 = (int)blockIdx.x * kSimpleRows, n1 = imin(s.n * G, n0 + kSimpleRows);
-    if (n0 >= n1) return;
-    for (int i = tid; i < kSimpleRows * D; i += blockDim.x) {
-        const int n = n0 + i / D;
-        qs[i] = n < n1 ? __bfloat162float(p.q[(size_t)(s.r0 + n / G) * p.q_stride + (size_t)(h * G + n % G) * D + i % D]) : 0.f;
-    }
-    const int p_first = s.kv - s.n + n0 / G, p_last = s.kv - s.n + (n1 - 1) / G;   // positions of the rows
-    const int k_end = imax(0, imin(s.kv, p_last + 1));
-    const int k_beg = p.window > 0 ? imax(0, p_first - p.window + 1) : 0;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[2][4] = {};
-    for (int k0 = k_beg; k0 < k_end; k0 += kSimpleKeys) {
-        __syncthreads();
-        for (int i = tid; i < kSimpleKeys * D; i += blockDim.x) {
-            const int kk = k0 + i / D, d = i % D;
-            float kx = 0.f, vx = 0.f;
-            if (kk < k_end) {
-                const int pid = c.table[(size_t)b * c.table_stride + kk / c.P];
-                if (pid < 0 || pid >= c.n_pages) {
-                    if (p.status) atomicExch(p.status, MASW_EINVAL);
-                } else {
-                    const size_t at = ((size_t)h * c.P + kk % c.P) * D + d, page = (size_t)pid * c.page_bytes;
-                    if (c.k_scale) {
-                        float hi;
-                        f16x2_to_f32(e4m3x2_to_f16x2(c.k[page + at]), kx, hi);
-                        f16x2_to_f32(e4m3x2_to_f16x2(c.v[page + at]), vx, hi);
-                        kx *= c.k_scale[(size_t)pid * c.Hkv + h];
-                        vx *= c.v_scale[(size_t)pid * c.Hkv + h];
-                    } else {
-                        kx = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(c.k + page)[at]);
-                        vx = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(c.v + page)[at]);
-                    }
-                }
-            }
-            ks[(i / D) * LD + d] = kx;
-            vs[(i / D) * LD + d] = vx;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-            const int n = n0 + warp * 2 + rr;
-            if (n >= n1) continue;
-            const int pos = s.kv - s.n + n / G, key = k0 + lane;
-            const bool see = key < k_end && key <= pos && (p.window <= 0 || key > pos - p.window);
-            float x = 0.f;
-            for (int d = 0; d < D; ++d) x = fmaf(qs[(n - n0) * D + d], ks[lane * LD + d], x);
-            x = see ? x * p.scale : -INFINITY;
-            float mx = x;
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float mn = fmaxf(m[rr], mx);
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            const float a = expf(m[rr] - ref), pr = see ? expf(x - ref) : 0.f;
-            float sum = pr;
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l[rr] = l[rr] * a + sum;
-            m[rr] = mn;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[rr][e] *= a;
-            for (int kk = 0; kk < kSimpleKeys; ++kk) {
-                const float w = __shfl_sync(0xffffffffu, pr, kk);
-                if (w == 0.f) continue;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (lane + 32 * e < D) acc[rr][e] = fmaf(w, vs[kk * LD + lane + 32 * e], acc[rr][e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
-        const int n = n0 + warp * 2 + rr;
-        if (n >= n1) continue;
-        const size_t row = (size_t)(s.r0 + n / G) * p.Hq + (size_t)h * G + n % G;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int d = lane + 32 * e;
-            if (d >= D) continue;
-            const float x = l[rr] == 0.f ? 0.f : acc[rr][e] / l[rr];
-            if (p.o_f32) ((float*)p.o)[row * D + d] = x;
-            else ((__nv_bfloat16*)p.o)[row * D + d] = __float2bfloat16_rn(x);
-        }
-        if (lane == 0 && p.lse) p.lse[row] = l[rr] == 0.f ? -INFINITY : m[rr] + logf(l[rr]);
-    }
+// The plan of the many-rows kernel: 128 / G tokens a tile, two tiles an item.  One
+// split, unless the items leave SMs without work: then as many as fill them once.
+static TilePlan tile_plan(const PagedView& c, int max_rows, int G, int sms) {
+    TilePlan t;
+    const int tokens = 2 * (kTile / G);
+    t.items = (max_rows + tokens - 1) / tokens;
+    const long long ctas = (long long)t.items * c.Hkv * c.B;
+    t.n_split = (int)std::max(1ll, std::min<long long>(64, sms / ctas));
+    return t;
 }
 
 }  // namespace masw
@@ -140,7 +51,10 @@ static int device_sms(int* sms) {
 }
 
 static size_t workspace_bytes_for(const PagedView& c, int max_rows, int G, int sms) {
-    if ((long long)max_rows * G > kRowsMax) return 16;
+    if ((long long)max_rows * G > kRowsMax) {
+        const TilePlan t = tile_plan(c, max_rows, G, sms);
+        return t.n_split == 1 ? 16 : (size_t)t.items * t.n_split * c.Hkv * c.B * 256 * (c.D + 2) * sizeof(float);
+    }
     return (size_t)sms * 2 * kRowsMax * (c.D + 2) * sizeof(float);   // two partials a CTA
 }
 
@@ -215,15 +129,14 @@ extern "C" int masw_paged_attn(const masw_paged_t* cache, const int* kv_len, con
     p.o_f32 = o_dtype == MASW_F32;
     p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)p.c.D);
     p.scale_log2 = p.scale * 1.4426950408889634f;
-    if (mr * p.G <= kRowsMax) {
-        const cudaError_t e = launch_paged_rows(p, sms, (cudaStream_t)stream);
-        if (e != cudaSuccess) return masw_set_error(nullptr, MASW_ECUDA, std::string("paged_attn: ") + cudaGetErrorString(e));
-        return MASW_OK;
+    cudaError_t e;
+    if ((long long)mr * p.G <= kRowsMax) {
+        e = launch_paged_rows(p, sms, (cudaStream_t)stream);
+    } else {
+        const TilePlan t = tile_plan(p.c, mr, p.G, sms);
+        if ((long long)t.items * 64 > 0x7fffffffll) return fail("max_rows too large");
+        e = launch_paged_tiles(p, t, (cudaStream_t)stream);
     }
-    const size_t smem = (size_t)(kSimpleRows * p.c.D + 2 * kSimpleKeys * (p.c.D + 1)) * sizeof(float);
-    const long long tiles = ((long long)mr * p.G + kSimpleRows - 1) / kSimpleRows;
-    const cudaError_t e = masw_launch(paged_attn_kernel, dim3((unsigned)tiles, p.c.Hkv, p.c.B), dim3(256), smem,
-                                      (cudaStream_t)stream, 1, p);
     if (e != cudaSuccess) return masw_set_error(nullptr, MASW_ECUDA, std::string("paged_attn: ") + cudaGetErrorString(e));
     return MASW_OK;
 }

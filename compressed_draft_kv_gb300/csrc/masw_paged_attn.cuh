@@ -32,6 +32,61 @@ __device__ __forceinline__ void store_out(const PagedAttnParams& p, size_t at, f
     else reinterpret_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
 }
 
+// wait_or_abort in few instructions: the kernel is large, and what stalled it most
+// was fetching instructions.  try_wait itself suspends the thread for a while.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    uint32_t n = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (++n == kWaitPolls) {
+            *abort_flag = 1;
+            atomicExch(err, MASW_ETIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// N consecutive fp32 columns (a multiple of 8) of this thread's TMEM lane
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* v) {
+    if constexpr (N >= 32) {
+        tc::tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld_cols<N - 32>(taddr + 32, v + 32);
+    } else if constexpr (N >= 16) {
+        tc::tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
+        tmem_ld_cols<N - 16>(taddr + 16, v + 16);
+    } else if constexpr (N >= 8) {
+        tc::tmem_ld8(taddr, *reinterpret_cast<uint32_t(*)[8]>(v));
+    }
+}
+
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// two f16 pairs -> four e4m3, rounded to nearest
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t h0, uint32_t h1) {
+    uint32_t r;
+    asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n mov.b32 %0, {a, b};\n}\n"
+        : "=r"(r)
+        : "r"(h0), "r"(h1));
+    return r;
+}
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t v, uint32_t& h0, uint32_t& h1) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(h0), "=r"(h1)
+        : "r"(v));
+}
+// h - e for a pair: what e4m3 left of it, exactly
+__device__ __forceinline__ uint32_t rest(uint32_t h, uint32_t e) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(e));
+    return r;
+}
+
 // The line of all pairs' tiles: pre[b] = tiles before sequence b, pre[B] = all
 // of them (returned), and the sequences' rows and lengths, by the whole CTA of NT
 // threads.  A sequence whose rows or length are not possible has no tiles.
@@ -83,6 +138,14 @@ __device__ int make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n
     __syncthreads();
     return total;
 }
+
+// How the many-rows kernel cuts its work: items of 256 rows a sequence, and splits
+// of an item's keys.
+struct TilePlan {
+    int items, n_split;
+};
+// The many-rows kernel and its merge (masw_paged_tile.cu).
+cudaError_t launch_paged_tiles(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st);
 
 // The few-rows kernel and its merge on n_cta CTAs (masw_paged_rows.cu).
 cudaError_t launch_paged_rows(const PagedAttnParams& p, int n_cta, cudaStream_t st);

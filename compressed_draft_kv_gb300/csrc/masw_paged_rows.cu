@@ -95,36 +95,6 @@ struct Cfg {
     static_assert(kKS + 2 < kMeta, "scales would be overwritten");
 };
 
-// wait_or_abort in few instructions: the kernel is large, and what stalled it most
-// was fetching instructions.  try_wait itself suspends the thread for a while.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
-    uint32_t n = 0;
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return false;
-        if (++n == kWaitPolls) {
-            *abort_flag = 1;
-            atomicExch(err, MASW_ETIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
-
-// N consecutive fp32 columns (a multiple of 8) of this thread's TMEM lane
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* v) {
-    if constexpr (N >= 32) {
-        tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld_cols<N - 32>(taddr + 32, v + 32);
-    } else if constexpr (N >= 16) {
-        tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
-        tmem_ld_cols<N - 16>(taddr + 16, v + 16);
-    } else if constexpr (N >= 8) {
-        tmem_ld8(taddr, *reinterpret_cast<uint32_t(*)[8]>(v));
-    }
-}
-
 // A CTA's walk over its tiles, piece by piece (a piece: tiles of one pair).
 struct Walk {
     int t, t1;               // tiles of the line left: [t, t1)
@@ -172,16 +142,6 @@ __device__ __forceinline__ float warp_max(float x) {   // in every lane; NaN doe
     return r;
 }
 
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t h) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-    return r;
-}
 // 16 (h - e) for a pair: what e4m3 left of it, exactly
 __device__ __forceinline__ uint32_t rest16(uint32_t h, uint32_t e) {
     uint32_t a, r;
@@ -717,10 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 #pragma unroll
                     for (int r = 0; r < NP; r += 4) {
                         const uint32_t h0 = cvt_f16x2(a[r], a[r + 1]), h1 = cvt_f16x2(a[r + 2], a[r + 3]);
-                        const uint32_t e0 = cvt_e4m3x2_f16x2(h0), e1 = cvt_e4m3x2_f16x2(h1);
-                        w[r / 4] = e0 | (e1 << 16);
-                        w[NP / 4 + r / 4] = cvt_e4m3x2_f16x2(rest16(h0, e4m3x2_to_f16x2(e0))) |
-                                            (cvt_e4m3x2_f16x2(rest16(h1, e4m3x2_to_f16x2(e1))) << 16);
+                        w[r / 4] = e4m3x4(h0, h1);
+                        uint32_t e0, e1;
+                        e4m3x4_to_f16x2(w[r / 4], e0, e1);
+                        w[NP / 4 + r / 4] = e4m3x4(rest16(h0, e0), rest16(h1, e1));
                     }
                 } else {
 #pragma unroll

@@ -1,0 +1,609 @@
+// Attention of many query rows a sequence over a paged cache (chunks of a prompt,
+// longer query blocks): 256 rows (query token x query head of the group) of a
+// (sequence, kv head) pair a CTA.
+//
+// A dense contraction, bound by the tensor cores once the rows share enough of
+// the cache: 4 D flops a row and visible key.  Two tiles of 128 rows go through
+// the keys together, 128 keys at a time, in turn: while the softmax of one tile
+// runs, the tensor cores work on the other one.  Per tile S = Q K^T (M = 128 rows,
+// N = 128 keys) and O += P V (N = head_dim) accumulate in tensor memory; two
+// threads own a row, one for each half of the keys.  (One thread a row spent 2000
+// cycles on a tile, and the tensor cores waited for it.)  P replaces S in tensor memory and is
+// the A operand of P V from there; matrix instructions of one thread run in the
+// order of their issue, so the next S follows the P V that reads P.
+// e4m3 pages enter as they are: Q as two e4m3 terms against the same K (twice the
+// instructions at twice the bf16 rate), the weights as two terms (off by at most
+// 2^-9) against the same V; the scales of a page multiply its columns of S and
+// enter the exponent as in the few-rows kernel.  bf16 pages: weights rounded to bf16
+// (2^-8 at most; the outputs are means over many of them).
+//
+// Warps 0-7 and 8-15: softmax of the two tiles; 16 and 17 issue their matrix
+// products (one warp for both blocked each tile behind the other's waits); 18: page
+// ids, scales and K; 19: page ids and V.  A long cache under few
+// rows is cut into splits, whose partial results a second kernel joins.
+#include "masw_paged_attn.cuh"
+
+namespace masw {
+namespace tile {
+
+using namespace tc;
+
+constexpr int kThreads = 640;
+constexpr int kMeta = 8;
+
+template <bool E4, int D>
+struct Cfg {
+    static constexpr int kES = E4 ? 1 : 2;
+    static constexpr int kRB = D * kES;
+    static constexpr int kPanels = kRB > 128 ? 2 : 1;
+    static constexpr int kPB = kRB / kPanels;
+    static constexpr uint32_t kPanel = kTile * kPB;
+    static constexpr uint32_t kTileB = kTile * kRB;
+    static constexpr uint32_t kSwz = kPB == 128 ? 2 : 4;
+    static constexpr uint32_t kAtom = 8 * kPB;
+    static constexpr int kTerms = E4 ? 2 : 1;                   // of Q and of the weights
+    static constexpr bool kWide = !E4 && D == 128;
+    static constexpr int kKS = kWide ? 3 : 4, kVS = kWide ? 2 : 4;
+    static constexpr uint32_t kOffQ = 0;                        // [2 tiles][terms]
+    static constexpr uint32_t kOffK = kOffQ + 2 * kTerms * kTileB;
+    static constexpr uint32_t kOffV = kOffK + kKS * kTileB;
+    static constexpr uint32_t kOffMeta = kOffV + kVS * kTileB;
+    static constexpr uint32_t kOffRow = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);   // a float per tile, half and row
+    static constexpr uint32_t kOffBar = kOffRow + 4 * kTile * 4;
+    static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kMetaBar = kVFree + kVS;
+    static constexpr int kSFull = kMetaBar + (E4 ? kMeta : 0), kPFull = kSFull + 2, kQFull = kPFull + 2, kOFull = kQFull + 2;
+    static constexpr int kDone = kOFull + 2, kBars = kDone + 2;
+    static constexpr uint32_t kSmem = kOffBar + 8 * kBars + 16;
+    static constexpr uint32_t kColS = 0, kColO = 256;           // per tile 128 columns of S (or P) and of O
+    static constexpr uint32_t kType = E4 ? 0 : 1;
+    static constexpr uint32_t kBase = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(kTile >> 4) << 24);
+    static constexpr uint32_t kIdescS = kBase | ((uint32_t)(kTile >> 3) << 17);
+    static constexpr uint32_t kIdescO = kBase | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+    static constexpr float kHead = E4 ? 7.f : 0.f;
+    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(kKS + 1 < kMeta, "scales would be overwritten");
+};
+
+// Barrier of the two warps (64 threads) that hold the same 32 rows, and their vote.
+__device__ __forceinline__ void bar_pair(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool bar_pair_or(int id, bool x) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)x), "r"(id)
+                 : "memory");
+    return r != 0;
+}
+
+// Item `item` of a sequence: tokens [tok0, tok1) of its rows, and the keys they see.
+struct Item {
+    int tok0, tok1, t0, nt;   // first key tile and number of tiles
+    int lo, hi;
+};
+__host__ __device__ inline Item item_of(int item, int n, int kv, int window, int tokens) {
+    Item x;
+    x.tok0 = item * 2 * tokens;
+    x.tok1 = x.tok0 + 2 * tokens < n ? x.tok0 + 2 * tokens : n;
+    const int first = kv - n + x.tok0, last = kv - n + x.tok1 - 1;   // positions
+    x.hi = last + 1 > 0 ? last + 1 : 0;
+    x.lo = window > 0 && first - window + 1 > 0 ? first - window + 1 : 0;
+    x.t0 = x.lo / kTile;
+    x.nt = (x.hi + kTile - 1) / kTile - x.t0;
+    if (x.nt < 1) x.nt = 1;
+    return x;
+}
+
+template <bool E4, int D>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ PagedAttnParams p, int n_split) {
+    using C = Cfg<E4, D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sb = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * C::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+    int* err_sink = reinterpret_cast<int*>(tslot + 2);
+    float4* meta = reinterpret_cast<float4*>(smem + C::kOffMeta);
+    auto bar_at = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
+    const PagedView& c = p.c;
+    const int G = p.G, tokens = kTile / G;   // tokens of a 128-row tile
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.z, h = blockIdx.y, Hkv = c.Hkv;
+    const int split = (int)blockIdx.x % n_split, n_items = (int)gridDim.x / n_split;
+    const int item = n_items - 1 - (int)blockIdx.x / n_split;   // the longest first
+    const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
+    if (!s.ok || s.n > p.max_rows || (sb & 1023u)) {
+        if (tid == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
+        return;
+    }
+    if (item * 2 * tokens >= s.n) return;
+    const Item it = item_of(item, s.n, s.kv, p.window, tokens);
+    const int chunk = (it.nt + n_split - 1) / n_split;
+    const int j0 = split * chunk, nt = imin(it.nt, j0 + chunk) - j0;   // this CTA's tiles
+    if (nt < 1) return;                                                // the merge knows
+    const int first_tile = it.t0 + j0;
+    const bool two = it.tok1 - it.tok0 > tokens;                       // the second tile has rows
+    int* const err = p.status ? p.status : err_sink;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tslot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < C::kBars; ++i)
+            mbar_init(bars + i, (i >= C::kPFull && i < C::kQFull + 2)                                                       ? 8
+                                : two && ((i >= C::kKFree && i < C::kVFull) || (i >= C::kVFree && i < C::kMetaBar)) ? 2
+                                                                                                                    : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    auto wait = [&](int bar, int phase) { return wait_bounded(bars + bar, (uint32_t)phase & 1u, abort_flag, err); };
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+    bool ok = true;
+
+    // 512 x 104 + 128 x 64 = 640 x 96 registers
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp < 18) {
+            // ---------------- matrix products of tile x ----------------
+            const int x = warp - 16;
+            if (x == 0 || two) {
+                const uint64_t aq = smem_desc(sb + C::kOffQ + x * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0);
+                const uint32_t ts = tmem + C::kColS + x * 128, to = tmem + C::kColO + x * 128;
+                ok = all(wait(C::kQFull + x, 0));
+                for (int j = 0; ok && j <= nt; ++j) {
+                    // what is there long before P is waited for first, so that P V and
+                    // the next S are issued without a pause
+                    const int ks = j % C::kKS, vs = (j - 1) % C::kVS;
+                    if (j < nt) ok = all(wait(C::kKFull + ks, j / C::kKS));
+                    if (j > 0) ok = ok && all(wait(C::kVFull + vs, (j - 1) / C::kVS)) && all(wait(C::kPFull + x, j - 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (j > 0) {
+                            const uint64_t bv = smem_desc(sb + C::kOffV + vs * C::kTileB, C::kPanel, C::kAtom, C::kSwz);
+                            constexpr int kKeys = 32 / C::kES;
+#pragma unroll
+                            for (int t = 0; t < C::kTerms; ++t)
+#pragma unroll
+                                for (int kk = 0; kk < kTile / kKeys; ++kk) {
+                                    const uint64_t bb = bv + (uint64_t)((kk * kKeys * C::kPB) >> 4);
+                                    const uint32_t acc = j > 1 || t > 0 || kk > 0;
+                                    if (E4) umma_f8_ts(to, ts + t * 32 + kk * 8, bb, C::kIdescO, acc);
+                                    else umma_bf16_ts(to, ts + t * 32 + kk * 8, bb, C::kIdescO, acc);
+                                }
+                            umma_commit(bar_at(C::kVFree + vs));
+                            if (j == nt) umma_commit(bar_at(C::kOFull + x));
+                        }
+                        if (j < nt) {
+                            const uint64_t bk = smem_desc(sb + C::kOffK + ks * C::kTileB, 16, C::kAtom, C::kSwz);
+#pragma unroll
+                            for (int t = 0; t < C::kTerms; ++t)
+#pragma unroll
+                                for (int kk = 0; kk < C::kRB / 32; ++kk) {
+                                    const uint64_t a = aq + (uint64_t)((t * C::kTileB + kk * 256) >> 4);
+                                    const uint64_t bb = bk + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
+                                    if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                                    else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                                }
+                            umma_commit(bar_at(C::kSFull + x));
+                            umma_commit(bar_at(C::kKFree + ks));
+                        }
+                    }
+                    __syncwarp();
+                }
+                // nothing may arrive on a barrier after the CTA ended
+                if (ok) ok = all(wait(C::kKFree + (nt - 1) % C::kKS, (nt - 1) / C::kKS)) && all(wait(C::kVFree + (nt - 1) % C::kVS, (nt - 1) / C::kVS));
+                if (!ok) {
+                    *abort_flag = 1;
+                    if (elect_one()) umma_commit(bar_at(C::kDone + x));
+                    __syncwarp();
+                    mbar_wait(bars + C::kDone + x, 0, nullptr);
+                }
+            }
+        } else {
+            // ---------------- page ids, scales, TMA: warp 18 K, warp 19 V ----------------
+            const bool is_v = warp == 19;
+            const int stages = is_v ? C::kVS : C::kKS, full = is_v ? C::kVFull : C::kKFull, freed = is_v ? C::kVFree : C::kKFree;
+            const uint32_t ring = sb + (is_v ? C::kOffV : C::kOffK);
+            const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
+            const bool scales = E4 && !is_v;
+            const int box = imin(c.P, kTile), bpt = kTile / box, bt = 32 / bpt;
+            const int key_lo = it.lo / c.P * c.P;    // first key of the first page with a visible key
+            auto load_ids = [&](int j, int& pid, bool& in) {   // the boxes of tiles j .. j + bt - 1
+                const int key = (first_tile + j) * kTile + lane * box;
+                in = j < nt && lane < imin(bt, nt - j) * bpt && key < it.hi && key >= key_lo;
+                pid = in ? __ldg(c.table + (size_t)b * c.table_stride + key / c.P) : 0;
+            };
+            auto check_and_scale = [&](int& pid, bool in, float& ks, float& vs) {
+                if (in && (pid < 0 || pid >= c.n_pages)) {
+                    atomicExch(err, MASW_EINVAL);
+                    pid = 0;
+                }
+                ks = vs = 1.f;
+                if (scales && in) {
+                    ks = __ldg(c.k_scale + (size_t)pid * Hkv + h);
+                    vs = __ldg(c.v_scale + (size_t)pid * Hkv + h);
+                }
+            };
+            int pid, pid1, pid2, st = 0, turn = 0, issued = 0;
+            bool in, in1, in2;
+            float ks, vs, ks1, vs1;
+            load_ids(0, pid, in);
+            load_ids(bt, pid1, in1);
+            check_and_scale(pid, in, ks, vs);
+            for (int base = 0; ok && base < nt; base += bt) {
+                check_and_scale(pid1, in1, ks1, vs1);
+                load_ids(base + 2 * bt, pid2, in2);
+                const float lvs = vs == 1.f ? 0.f : __log2f(vs), ivs = __frcp_rn(vs);
+                for (int j = base; j < imin(nt, base + bt); ++j) {
+                    if (turn > 0) ok = all(wait(freed + st, turn - 1));
+                    if (!ok) break;
+                    const int q0 = (j - base) * bpt;
+                    const uint32_t boxes = __ballot_sync(0xffffffffu, in) >> q0 & (bpt == 32 ? 0xffffffffu : (1u << bpt) - 1u);
+                    if (scales) {
+                        if (lane >= q0 && lane < q0 + bpt) meta[(j % kMeta) * 8 + lane - q0] = make_float4(ks, lvs, ivs, 0.f);
+                        __syncwarp();
+                    }
+                    if (elect_one()) {
+                        if (scales) mbar_arrive(bar_at(C::kMetaBar + j % kMeta));
+                        mbar_expect_tx(bars + full + st, (uint32_t)(__popc(boxes) * box * C::kRB));
+                    }
+                    __syncwarp();
+                    for (int q = 0; q < bpt; ++q) {
+                        const int id = __shfl_sync(0xffffffffu, pid, q0 + q);
+                        const int row = ((first_tile + j) * kTile + q * box) & (c.P - 1);
+                        const uint32_t dst = ring + st * C::kTileB + (uint32_t)(q * box * C::kPB);
+                        if ((boxes >> q & 1u) && elect_one()) {
+#pragma unroll
+                            for (int pn = 0; pn < C::kPanels; ++pn)
+                                tma_load_4d(dst + pn * C::kPanel, map, pn * C::kPB / C::kES, row, h, id, bar_at(full + st));
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++st == stages) {
+                        st = 0;
+                        ++turn;
+                    }
+                }
+                pid = pid1;
+                in = in1;
+                ks = ks1;
+                vs = vs1;
+                pid1 = pid2;
+                in1 = in2;
+            }
+            if (!ok) *abort_flag = 1;
+            for (int k = imax(0, issued - stages); k < issued; ++k)
+                mbar_wait(bars + full + k % stages, (uint32_t)(k / stages) & 1u, nullptr);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        // ---------------- softmax: row r of tile x, keys 64 hf .. 64 hf + 63 of each tile of keys ----------------
+        const int x = warp >> 3, hf = (warp >> 2) & 1, r = tid & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + C::kColS + x * 128 + lane_off, t_o = tmem + C::kColO + x * 128 + lane_off;
+        const int pair = 1 + x * 4 + (warp & 3);                          // barrier of the two warps that share 32 rows
+        float* mine = reinterpret_cast<float*>(smem + C::kOffRow) + (x * 2 + hf) * kTile + r;
+        const float* other = mine + (hf ? -kTile : kTile);
+        const int tok_first = it.tok0 + x * tokens;                       // of the tile
+        const int tok_last = imin(it.tok1, tok_first + tokens) - 1;
+        const int tok = imin(tok_first + r / G, tok_last), g = r % G;
+        const bool live = r < (tok_last - tok_first + 1) * G;             // rows behind repeat the last token
+        const int pos = s.kv - s.n + tok;
+        const size_t row = (size_t)(s.r0 + tok) * p.Hq + (size_t)h * G + g;
+        if (x == 0 || two) {
+            // Q: this row's half, split into its terms
+            float qs = 1.f;
+            {
+                const __nv_bfloat16* src = p.q + (size_t)(s.r0 + tok) * p.q_stride + (size_t)(h * G + g) * D + hf * (D / 2);
+                const uint32_t dst = sb + C::kOffQ + x * C::kTerms * C::kTileB + (uint32_t)((r >> 3) * (C::kRB / 16) * 128 + (r & 7) * 16) +
+                                     (uint32_t)(hf * (C::kRB / 32) * 128);
+                uint4 q[D / 16];
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
+                if constexpr (E4) {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        float f[8];
+                        Elem<__nv_bfloat16>::unpack(q[k], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
+                    }
+                    *mine = amax;
+                    bar_pair(pair);
+                    qs = pow2_scale(fmaxf(amax, *other));
+                    const float inv = 1.f / qs;
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t w1[4], w2[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4& v = q[2 * k + e / 2];
+                            const uint32_t lo = e & 1 ? v.z : v.x, hi = e & 1 ? v.w : v.y;
+                            const float f[4] = {bf16lo(lo) * inv, bf16hi(lo) * inv, bf16lo(hi) * inv, bf16hi(hi) * inv};
+                            const uint32_t a = e4m3x2(f[0], f[1]), bq = e4m3x2(f[2], f[3]);
+                            float d0, d1, d2, d3;
+                            f16x2_to_f32(e4m3x2_to_f16x2(a), d0, d1);
+                            f16x2_to_f32(e4m3x2_to_f16x2(bq), d2, d3);
+                            w1[e] = a | (bq << 16);
+                            w2[e] = e4m3x2(f[0] - d0, f[1] - d1) | (e4m3x2(f[2] - d2, f[3] - d3) << 16);
+                        }
+                        st_shared_v4(dst + k * 128, w1[0], w1[1], w1[2], w1[3]);
+                        st_shared_v4(dst + C::kTileB + k * 128, w2[0], w2[1], w2[2], w2[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) st_shared_v4(dst + k * 128, q[k].x, q[k].y, q[k].z, q[k].w);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_at(C::kQFull + x));
+            }
+            const float qk = qs * p.scale_log2;
+            const int row_lo = p.window > 0 ? imax(0, pos - p.window + 1) : 0;
+            // keys that every row of the tile sees
+            const int all_hi = s.kv - s.n + tok_first + 1;
+            const int all_lo = p.window > 0 ? imax(0, s.kv - s.n + tok_last - p.window + 1) : 0;
+            // 16 columns lie in one page: its scales
+            const int page_shift = __ffs(imin(c.P, kTile)) - 1 - 4;
+            float mref = -INFINITY, l = 0.f;   // the row's reference (the same in both threads) and this half's sum
+            for (int j = 0; j < nt; ++j) {
+                const int tile0 = (first_tile + j) * kTile;
+                // rows of V that no row of the item sees must not reach the product
+                // (both tiles clear them: each before its own product)
+                if (hf == 0 && (tile0 < it.lo || tile0 + kTile > it.hi)) {
+                    ok &= wait(C::kVFull + j % C::kVS, j / C::kVS);
+                    if (tile0 + r < it.lo || tile0 + r >= it.hi) {
+#pragma unroll
+                        for (int pn = 0; pn < C::kPanels; ++pn)
+#pragma unroll
+                            for (int q = 0; q < C::kPB / 16; ++q)
+                                st_shared_v4(sb + C::kOffV + (j % C::kVS) * C::kTileB + pn * C::kPanel + r * C::kPB + q * 16, 0u, 0u, 0u, 0u);
+                    }
+                    fence_async_smem();
+                }
+                if (E4) ok &= wait(C::kMetaBar + j % kMeta, j / kMeta);
+                ok &= wait(C::kSFull + x, j);
+                __syncwarp();
+                tc_fence_after();
+                constexpr int kCols = kTile / 2;
+                float a[kCols];
+                tmem_ld_cols<kCols>(t_s + hf * kCols, reinterpret_cast<uint32_t*>(a));
+                tmem_wait_ld();
+                const bool masked = tile0 < all_lo || tile0 + kTile > all_hi;
+                const int see_lo = row_lo - tile0 - hf * kCols, see_hi = pos + 1 - tile0 - hf * kCols;   // columns the row sees
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e) a[e] = e >= see_lo && e < see_hi ? a[e] : -INFINITY;
+                }
+                const uint32_t ma = sb + C::kOffMeta + (j % kMeta) * 128u;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < kCols / 16; ++q) {
+                    float m0 = fmax3(a[q * 16], a[q * 16 + 1], a[q * 16 + 2]), m1 = fmax3(a[q * 16 + 3], a[q * 16 + 4], a[q * 16 + 5]);
+#pragma unroll
+                    for (int e = 6; e < 14; e += 4) {
+                        m0 = fmax3(m0, a[q * 16 + e], a[q * 16 + e + 1]);
+                        m1 = fmax3(m1, a[q * 16 + e + 2], a[q * 16 + e + 3]);
+                    }
+                    m0 = fmax3(m0, m1, fmaxf(a[q * 16 + 14], a[q * 16 + 15]));
+                    if (E4) {
+                        const float4 sc = ld_shared_v4f(ma + (uint32_t)((hf * 4 + q) >> page_shift) * 16u);
+                        m0 = m0 == -INFINITY ? m0 : fmaf(m0, qk * sc.x, sc.y);
+                    } else {
+                        m0 *= qk;
+                    }
+                    mx = fmaxf(mx, m0);
+                }
+                // the row's reference moves when a score of either half exceeds it by
+                // more than 2^8; the vote also says that both halves of S were read,
+                // which P overwrites
+                if (bar_pair_or(pair, mx - mref > 8.f)) {
+                    *mine = mx;
+                    bar_pair(pair);
+                    const float top = fmaxf(mx, *other);
+                    float alpha = 1.f;
+                    if (top - mref > 8.f) {
+                        const float up = top - C::kHead;
+                        alpha = ex2_approx(mref - up);
+                        mref = up;
+                        l *= alpha;
+                    }
+                    if (j > 0) {
+                        // S(j) done means that P V of the tile before it is; this thread
+                        // scales its half of the row's O
+#pragma unroll 1
+                        for (int q = hf * (D / 2); q < (hf + 1) * (D / 2); q += 16) {
+                            uint32_t ov[16];
+                            tmem_ld16(t_o + q, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            tmem_st16(t_o + q, ov);
+                        }
+                        tmem_wait_st();
+                    }
+                    bar_pair(pair);   // the maxima were read
+                }
+                const float nref = mref == -INFINITY ? 0.f : mref;
+                uint32_t w1[E4 ? 8 : 16], w2[8];   // terms of 32 columns
+#pragma unroll
+                for (int q = 0; q < kCols / 16; ++q) {
+                    float ks = qk, add = -nref, ivs = 1.f;
+                    if (E4) {
+                        const float4 sc = ld_shared_v4f(ma + (uint32_t)((hf * 4 + q) >> page_shift) * 16u);
+                        ks = qk * sc.x;
+                        add = sc.y - nref;
+                        ivs = sc.z;
+                        // where the row sees nothing of the page, its scales may be anything
+                        if (masked && !(q * 16 + 16 > see_lo && q * 16 < see_hi)) {
+                            ks = ivs = 1.f;
+                            add = 0.f;
+                        }
+                    }
+                    const uint64_t ks2 = f2_pack(ks, ks), add2 = f2_pack(add, add);
+                    uint64_t sum2 = 0;
+                    uint32_t hw[8];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float u, v;
+                        f2_unpack(f2_fma(f2_pack(a[q * 16 + e], a[q * 16 + e + 1]), ks2, add2), u, v);
+                        u = ex2_approx(u);
+                        v = ex2_approx(v);
+                        sum2 = f2_add(sum2, f2_pack(u, v));
+                        hw[e / 2] = E4 ? cvt_f16x2(u, v) : pack_bf16(u, v);
+                    }
+                    float s0, s1;
+                    f2_unpack(sum2, s0, s1);
+                    l = E4 ? fmaf(s0 + s1, ivs, l) : l + (s0 + s1);
+                    if constexpr (E4) {
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const uint32_t t = e4m3x4(hw[e], hw[e + 1]);
+                            uint32_t e0, e1;
+                            e4m3x4_to_f16x2(t, e0, e1);
+                            w1[(q & 1) * 4 + e / 2] = t;
+                            w2[(q & 1) * 4 + e / 2] = e4m3x4(rest(hw[e], e0), rest(hw[e + 1], e1));
+                        }
+                        if (q & 1) {
+                            tmem_st8(t_s + hf * 16 + (q >> 1) * 8, w1);
+                            tmem_st8(t_s + 32 + hf * 16 + (q >> 1) * 8, w2);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w1[(q & 1) * 8 + e] = hw[e];
+                        if (q & 1) tmem_st16(t_s + hf * 32 + (q >> 1) * 16, w1);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_at(C::kPFull + x));
+            }
+            *mine = l;
+            bar_pair(pair);
+            l += *other;
+            ok &= wait(C::kOFull + x, 0);
+            __syncwarp();
+            tc_fence_after();
+            float* part = nullptr;
+            if (n_split > 1) {
+                const size_t unit = ((size_t)(b * Hkv + h) * n_items + item) * n_split + split;
+                part = p.part + unit * 256 * (D + 2) + (size_t)(x * 128 + r) * (D + 2);
+                if (live && hf == 0) {
+                    __stcg(part + D, l == 0.f ? -INFINITY : mref);
+                    __stcg(part + D + 1, l);
+                }
+            } else if (live && hf == 0 && p.lse) {
+                p.lse[row] = l == 0.f ? -INFINITY : (mref + __log2f(l)) * 0.6931471805599453f;
+            }
+            const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll 1
+            for (int q = hf * (D / 2); q < (hf + 1) * (D / 2); q += 32) {
+                uint32_t ov[32];
+                tmem_ld32(t_o + q, ov);
+                tmem_wait_ld();
+                if (!live) continue;
+                if (part || p.o_f32) {
+                    float* dst = part ? part + q : reinterpret_cast<float*>(p.o) + row * D + q;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        __stcg(reinterpret_cast<float2*>(dst + e), make_float2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv));
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = pack_bf16(__uint_as_float(ov[8 * e + 2 * k]) * inv, __uint_as_float(ov[8 * e + 2 * k + 1]) * inv);
+                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (!ok) *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// Joins the splits of every row: a warp a row, D / 32 elements a lane.
+template <int D>
+__global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__ PagedAttnParams p, int n_split, int n_items) {
+    const PagedView& c = p.c;
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.z, h = blockIdx.y, G = p.G, tokens = kTile / G, lane = threadIdx.x & 31;
+    const int item = (int)blockIdx.x / 32, r = ((int)blockIdx.x % 32) * 8 + (int)(threadIdx.x >> 5);   // row of the 256
+    const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
+    if (!s.ok || s.n > p.max_rows || item * 2 * tokens >= s.n) return;
+    const Item it = item_of(item, s.n, s.kv, p.window, tokens);
+    const int tok = it.tok0 + (r >> 7) * tokens + (r & 127) / G;
+    if ((r & 127) >= tokens * G || tok >= it.tok1) return;
+    const int chunk = (it.nt + n_split - 1) / n_split;
+    constexpr int kE = D / 32;
+    float M = -INFINITY, l = 0.f, o[kE] = {};
+    const size_t unit = ((size_t)(b * c.Hkv + h) * n_items + item) * n_split;
+    for (int q = 0; q < n_split && q * chunk < it.nt; ++q) {
+        const float* part = p.part + (unit + q) * 256 * (D + 2) + (size_t)r * (D + 2);
+        const float m = __ldcg(part + D), pl = __ldcg(part + D + 1);
+        float v[kE];
+#pragma unroll
+        for (int e = 0; e < kE; e += 2) {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(part + lane * kE + e));
+            v[e] = f.x;
+            v[e + 1] = f.y;
+        }
+        if (m == -INFINITY) continue;
+        const float nm = fmaxf(M, m), w0 = exp2f(M - nm), w1 = exp2f(m - nm);
+        l = l * w0 + pl * w1;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = o[e] * w0 + v[e] * w1;
+        M = nm;
+    }
+    const size_t row = (size_t)(s.r0 + tok) * p.Hq + (size_t)h * G + (r & 127) % G;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) store_out(p, row * D + lane * kE + e, l == 0.f ? 0.f : o[e] / l);
+    if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+}
+
+template <bool E4, int D>
+cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st) {
+    using C = Cfg<E4, D>;
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!configured[dev & 63].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(tile_kernel<E4, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        configured[dev & 63].store(true, std::memory_order_release);
+    }
+    e = masw_launch(tile_kernel<E4, D>, dim3(plan.items * plan.n_split, p.c.Hkv, p.c.B), dim3(kThreads), C::kSmem, st, 1, p, plan.n_split);
+    if (e != cudaSuccess || plan.n_split == 1) return e;
+    return masw_launch(tile_merge_kernel<D>, dim3(plan.items * 32, p.c.Hkv, p.c.B), dim3(256), 0, st, 1, p, plan.n_split, plan.items);
+}
+
+}  // namespace tile
+
+cudaError_t launch_paged_tiles(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st) {
+    if (p.c.k_scale) return p.c.D == 64 ? tile::launch<true, 64>(p, plan, st) : tile::launch<true, 128>(p, plan, st);
+    return p.c.D == 64 ? tile::launch<false, 64>(p, plan, st) : tile::launch<false, 128>(p, plan, st);
+}
+
+}  // namespace masw

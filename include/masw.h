@@ -407,9 +407,10 @@ int masw_paged_append(const masw_paged_t* cache, const int* kv_len, const int* r
  * A non-finite value at a key that a sequence's queries partly see may reach those
  * of its rows that share a tile with a row that sees it.
  * Scores, softmax statistics and sums are fp32.  With e4m3 pages Q enters the
- * matrix products as two e4m3 terms (exact but for what lies 2^-21 below the
- * largest element among a pair's rows) and each weight as three, of its fp16
- * value; with bf16 pages a weight enters as bf16 terms.
+ * matrix products as two e4m3 terms (exact but for what lies 2^-18 below the
+ * largest element of its row, or of the pair's rows when they are few) and so does
+ * each weight (off by at most 2^-9 of itself or 2^-16 of the largest); with bf16
+ * pages a weight enters as bf16.
  * workspace: device scratch of masw_paged_workspace_bytes() bytes, 16-byte
  * aligned; needs no initialisation and must not be shared by calls that overlap on
  * the GPU.  status: device int or NULL; the call writes there MASW_EINVAL for a
