@@ -80,13 +80,6 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t v, uint32_t& h0, uint32
         : "=r"(h0), "=r"(h1)
         : "r"(v));
 }
-// h - e for a pair: what e4m3 left of it, exactly
-__device__ __forceinline__ uint32_t rest(uint32_t h, uint32_t e) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(e));
-    return r;
-}
-
 // The line of all pairs' tiles: pre[b] = tiles before sequence b, pre[B] = all
 // of them (returned), and the sequences' rows and lengths, by the whole CTA of NT
 // threads.  A sequence whose rows or length are not possible has no tiles.

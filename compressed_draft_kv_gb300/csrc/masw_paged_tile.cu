@@ -11,15 +11,22 @@
 // cycles on a tile, and the tensor cores waited for it.)  P replaces S in tensor memory and is
 // the A operand of P V from there; matrix instructions of one thread run in the
 // order of their issue, so the next S follows the P V that reads P.
-// e4m3 pages enter as they are: Q as two e4m3 terms against the same K (twice the
-// instructions at twice the bf16 rate), the weights as two terms (off by at most
-// 2^-9) against the same V; the scales of a page multiply its columns of S and
-// enter the exponent as in the few-rows kernel.  bf16 pages: weights rounded to bf16
-// (2^-8 at most; the outputs are means over many of them).
+// e4m3 pages: K enters as it is, against Q as two e4m3 terms (twice the instructions
+// at twice the bf16 rate); V is widened to fp16 in shared memory, which is exact,
+// once for both tiles, so that the weights enter as fp16 (off by at most 2^-11):
+// splitting the weights into e4m3 terms instead took a third of the softmax's
+// instructions.  The scales of a page multiply its columns of S and enter the
+// exponent as in the few-rows kernel.  bf16 pages: weights rounded to bf16 (2^-8 at
+// most; the outputs are means over many of them).
 //
-// Warps 0-7 and 8-15: softmax of the two tiles; 16 and 17 issue their matrix
-// products (one warp for both blocked each tile behind the other's waits); 18: page
-// ids, scales and K; 19: page ids and V.  A long cache under few
+// Warps 0-7 and 8-15: softmax of the two tiles; 16 issues the matrix products of
+// whichever tile is ready, all of a tile's at once: P V and the next S of one tile
+// run while the other one's softmax does (in a fixed order each tile waited behind
+// the other; with an issuing warp a tile the products of both interleaved, ended
+// together, and left the tensor cores idle during both softmaxes); 17 watches K and V
+// for it.  18: page ids,
+// scales and K; 19: page ids and V; 20-23 widen V and clear the rows that no query
+// sees.  A long cache under few
 // rows is cut into splits, whose partial results a second kernel joins.
 #include "masw_paged_attn.cuh"
 
@@ -28,7 +35,7 @@ namespace tile {
 
 using namespace tc;
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr int kMeta = 8;
 
 template <bool E4, int D>
@@ -41,25 +48,30 @@ struct Cfg {
     static constexpr uint32_t kTileB = kTile * kRB;
     static constexpr uint32_t kSwz = kPB == 128 ? 2 : 4;
     static constexpr uint32_t kAtom = 8 * kPB;
-    static constexpr int kTerms = E4 ? 2 : 1;                   // of Q and of the weights
-    static constexpr bool kWide = !E4 && D == 128;
-    static constexpr int kKS = kWide ? 3 : 4, kVS = kWide ? 2 : 4;
+    static constexpr int kTerms = E4 ? 2 : 1;                   // of Q
+    static constexpr int kKS = 3, kVS = 2;                      // stages of K and V
+    static constexpr int kWS = 2;                               // buffers of V as the products read it (bf16: the stages)
+    // V as the products read it, 2 bytes an element: panels of 64 elements
+    static constexpr int kWPanels = D / 64;
+    static constexpr uint32_t kWPanel = kTile * 128;
+    static constexpr uint32_t kWideB = kWPanels * kWPanel;
     static constexpr uint32_t kOffQ = 0;                        // [2 tiles][terms]
     static constexpr uint32_t kOffK = kOffQ + 2 * kTerms * kTileB;
     static constexpr uint32_t kOffV = kOffK + kKS * kTileB;
-    static constexpr uint32_t kOffMeta = kOffV + kVS * kTileB;
+    static constexpr uint32_t kOffW = E4 ? kOffV + kVS * kTileB : kOffV;
+    static constexpr uint32_t kOffMeta = kOffW + kWS * kWideB;
     static constexpr uint32_t kOffRow = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);   // a float per tile, half and row
     static constexpr uint32_t kOffBar = kOffRow + 4 * kTile * 4;
-    static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kMetaBar = kVFree + kVS;
-    static constexpr int kSFull = kMetaBar + (E4 ? kMeta : 0), kPFull = kSFull + 2, kQFull = kPFull + 2, kOFull = kQFull + 2;
-    static constexpr int kDone = kOFull + 2, kBars = kDone + 2;
+    static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kWFull = kVFree + kVS, kWFree = kWFull + kWS, kMetaBar = kWFree + kWS;
+    static constexpr int kSFull = kMetaBar + (E4 ? kMeta : 0), kGo = kSFull + 2, kOFull = kGo + 2;   // kGo: all that a step of a tile needs
+    static constexpr int kDone = kOFull + 2, kBars = kDone + 1;
     static constexpr uint32_t kSmem = kOffBar + 8 * kBars + 16;
     static constexpr uint32_t kColS = 0, kColO = 256;           // per tile 128 columns of S (or P) and of O
     static constexpr uint32_t kType = E4 ? 0 : 1;
     static constexpr uint32_t kBase = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(kTile >> 4) << 24);
     static constexpr uint32_t kIdescS = kBase | ((uint32_t)(kTile >> 3) << 17);
-    static constexpr uint32_t kIdescO = kBase | (1u << 16) | ((uint32_t)(D >> 3) << 17);
-    static constexpr float kHead = E4 ? 7.f : 0.f;
+    static constexpr uint32_t kIdescO = (1u << 4) | ((E4 ? 0u : 1u) << 7) | ((E4 ? 0u : 1u) << 10) | ((uint32_t)(kTile >> 4) << 24) |
+                                        (1u << 16) | ((uint32_t)(D >> 3) << 17);   // fp16 or bf16
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(kKS + 1 < kMeta, "scales would be overwritten");
 };
@@ -93,7 +105,8 @@ __host__ __device__ inline Item item_of(int item, int n, int kv, int window, int
     return x;
 }
 
-template <bool E4, int D>
+// NS: pages that half a tile of keys (64) touches, as far as scales go: 1, 2 or 4
+template <bool E4, int D, int NS>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ PagedAttnParams p, int n_split) {
     using C = Cfg<E4, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -132,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     if (tid == 0) {
         for (int i = 0; i < C::kBars; ++i)
-            mbar_init(bars + i, (i >= C::kPFull && i < C::kQFull + 2)                                                       ? 8
+            mbar_init(bars + i, i >= C::kGo && i < C::kGo + 2                                                                ? 9
+                                : (i >= C::kWFull && i < C::kWFree) || (E4 && i >= C::kVFree && i < C::kWFull)    ? 4
                                 : two && ((i >= C::kKFree && i < C::kVFull) || (i >= C::kVFree && i < C::kMetaBar)) ? 2
                                                                                                                     : 1);
         *abort_flag = 0;
@@ -146,67 +160,79 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     bool ok = true;
 
-    // 512 x 104 + 128 x 64 = 640 x 96 registers
+    // 512 x 96 + 256 x 48 = 768 x 80 registers
     if (warp >= 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp < 18) {
-            // ---------------- matrix products of tile x ----------------
-            const int x = warp - 16;
-            if (x == 0 || two) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 16) {
+            // ---------------- matrix products ----------------
+            auto ready = [&](int bar, int phase) { return all(mbar_test(bars + bar, (uint32_t)phase & 1u)); };
+            int next[2] = {0, two ? 0 : nt + 1};   // per tile: step j is P V of tile j - 1 and S of tile j
+            uint32_t polls = 0;
+            for (int x = 0; ok && (next[0] <= nt || next[1] <= nt); x ^= 1) {
+                const int j = x ? next[1] : next[0];
+                if (j > nt) continue;
+                if (!ready(C::kGo + x, j)) {
+                    if (all(*abort_flag != 0)) ok = false;
+                    if (++polls == kWaitPolls) {
+                        atomicExch(err, MASW_ETIMEOUT);
+                        ok = false;
+                    }
+                    continue;
+                }
+                const int ks = j % C::kKS, ws = (j - 1) % C::kWS;
+                polls = 0;
+                tc_fence_after();
                 const uint64_t aq = smem_desc(sb + C::kOffQ + x * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0);
                 const uint32_t ts = tmem + C::kColS + x * 128, to = tmem + C::kColO + x * 128;
-                ok = all(wait(C::kQFull + x, 0));
-                for (int j = 0; ok && j <= nt; ++j) {
-                    // what is there long before P is waited for first, so that P V and
-                    // the next S are issued without a pause
-                    const int ks = j % C::kKS, vs = (j - 1) % C::kVS;
-                    if (j < nt) ok = all(wait(C::kKFull + ks, j / C::kKS));
-                    if (j > 0) ok = ok && all(wait(C::kVFull + vs, (j - 1) / C::kVS)) && all(wait(C::kPFull + x, j - 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (j > 0) {
-                            const uint64_t bv = smem_desc(sb + C::kOffV + vs * C::kTileB, C::kPanel, C::kAtom, C::kSwz);
-                            constexpr int kKeys = 32 / C::kES;
+                if (elect_one()) {
+                    if (j > 0) {
+                        const uint64_t bv = smem_desc(sb + C::kOffW + ws * C::kWideB, C::kWPanel, 1024, 2);
 #pragma unroll
-                            for (int t = 0; t < C::kTerms; ++t)
-#pragma unroll
-                                for (int kk = 0; kk < kTile / kKeys; ++kk) {
-                                    const uint64_t bb = bv + (uint64_t)((kk * kKeys * C::kPB) >> 4);
-                                    const uint32_t acc = j > 1 || t > 0 || kk > 0;
-                                    if (E4) umma_f8_ts(to, ts + t * 32 + kk * 8, bb, C::kIdescO, acc);
-                                    else umma_bf16_ts(to, ts + t * 32 + kk * 8, bb, C::kIdescO, acc);
-                                }
-                            umma_commit(bar_at(C::kVFree + vs));
-                            if (j == nt) umma_commit(bar_at(C::kOFull + x));
-                        }
-                        if (j < nt) {
-                            const uint64_t bk = smem_desc(sb + C::kOffK + ks * C::kTileB, 16, C::kAtom, C::kSwz);
-#pragma unroll
-                            for (int t = 0; t < C::kTerms; ++t)
-#pragma unroll
-                                for (int kk = 0; kk < C::kRB / 32; ++kk) {
-                                    const uint64_t a = aq + (uint64_t)((t * C::kTileB + kk * 256) >> 4);
-                                    const uint64_t bb = bk + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
-                                    if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
-                                    else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
-                                }
-                            umma_commit(bar_at(C::kSFull + x));
-                            umma_commit(bar_at(C::kKFree + ks));
-                        }
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            umma_bf16_ts(to, ts + kk * 8, bv + (uint64_t)((kk * 2048) >> 4), C::kIdescO, j > 1 || kk > 0);
+                        umma_commit(bar_at((E4 ? C::kWFree : C::kVFree) + ws));
+                        if (j == nt) umma_commit(bar_at(C::kOFull + x));
                     }
-                    __syncwarp();
+                    if (j < nt) {
+                        const uint64_t bk = smem_desc(sb + C::kOffK + ks * C::kTileB, 16, C::kAtom, C::kSwz);
+#pragma unroll
+                        for (int t = 0; t < C::kTerms; ++t)
+#pragma unroll
+                            for (int kk = 0; kk < C::kRB / 32; ++kk) {
+                                const uint64_t a = aq + (uint64_t)((t * C::kTileB + kk * 256) >> 4);
+                                const uint64_t bb = bk + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
+                                if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                                else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                            }
+                        umma_commit(bar_at(C::kSFull + x));
+                        umma_commit(bar_at(C::kKFree + ks));
+                    }
                 }
-                // nothing may arrive on a barrier after the CTA ended
-                if (ok) ok = all(wait(C::kKFree + (nt - 1) % C::kKS, (nt - 1) / C::kKS)) && all(wait(C::kVFree + (nt - 1) % C::kVS, (nt - 1) / C::kVS));
-                if (!ok) {
-                    *abort_flag = 1;
-                    if (elect_one()) umma_commit(bar_at(C::kDone + x));
-                    __syncwarp();
-                    mbar_wait(bars + C::kDone + x, 0, nullptr);
+                __syncwarp();
+                if (x) ++next[1];
+                else ++next[0];
+            }
+            // nothing may arrive on a barrier after the CTA ended
+            if (ok) ok = all(wait(C::kKFree + (nt - 1) % C::kKS, (nt - 1) / C::kKS)) && all(wait((E4 ? C::kWFree : C::kVFree) + (nt - 1) % C::kWS, (nt - 1) / C::kWS));
+            if (!ok) {
+                *abort_flag = 1;
+                if (elect_one()) umma_commit(bar_at(C::kDone));
+                __syncwarp();
+                mbar_wait(bars + C::kDone, 0, nullptr);
+            }
+        } else if (warp == 17) {
+            // ---------------- K and V there: the ninth arrival on a step's barrier ----------------
+            // (a test takes ~100 cycles: the issuing warp is left with one a step)
+            for (int j = 0; ok && j <= nt; ++j) {
+                if (j < nt) ok = all(wait(C::kKFull + j % C::kKS, j / C::kKS));
+                if (j > 0) ok = ok && all(wait(C::kWFull + (j - 1) % C::kWS, (j - 1) / C::kWS));
+                for (int x = 0; ok && x < (two ? 2 : 1); ++x) {
+                    if (j > 0) ok = all(wait(C::kGo + x, j - 1));   // one arrival a phase
+                    if (ok && lane == 0) mbar_arrive(bar_at(C::kGo + x));
                 }
             }
-        } else {
+            if (!ok) *abort_flag = 1;
+        } else if (warp < 20) {
             // ---------------- page ids, scales, TMA: warp 18 K, warp 19 V ----------------
             const bool is_v = warp == 19;
             const int stages = is_v ? C::kVS : C::kKS, full = is_v ? C::kVFull : C::kKFull, freed = is_v ? C::kVFree : C::kKFree;
@@ -282,10 +308,52 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             if (!ok) *abort_flag = 1;
             for (int k = imax(0, issued - stages); k < issued; ++k)
                 mbar_wait(bars + full + k % stages, (uint32_t)(k / stages) & 1u, nullptr);
+        } else {
+            // ---------------- V as the products read it: thread t row t of the tile ----------------
+            const int t = tid & 127;
+            for (int j = 0; ok && j < nt; ++j) {
+                const int key = (first_tile + j) * kTile + t, st = j % C::kVS;
+                const bool seen = key >= it.lo && key < it.hi;   // by some row; a row that none sees must not reach the product
+                ok = all(wait(C::kVFull + st, j / C::kVS));
+                if (E4 && j >= C::kWS) ok = ok && all(wait(C::kWFree + j % C::kWS, j / C::kWS - 1));
+                if (!ok) break;
+                const uint32_t dst = sb + C::kOffW + (j % C::kWS) * C::kWideB + t * 128;
+                if constexpr (E4) {
+                    const uint32_t src = sb + C::kOffV + st * C::kTileB + t * C::kPB;
+                    const int swz = D == 128 ? t & 7 : (t >> 1) & 3;
+#pragma unroll
+                    for (int q = 0; q < D / 16; ++q) {
+                        const float4 f = ld_shared_v4f(src + ((uint32_t)(q ^ swz) << 4));
+                        uint32_t w[8];
+                        e4m3x4_to_f16x2(__float_as_uint(f.x), w[0], w[1]);
+                        e4m3x4_to_f16x2(__float_as_uint(f.y), w[2], w[3]);
+                        e4m3x4_to_f16x2(__float_as_uint(f.z), w[4], w[5]);
+                        e4m3x4_to_f16x2(__float_as_uint(f.w), w[6], w[7]);
+                        if (!seen)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) w[e] = 0u;
+                        const uint32_t at = dst + (uint32_t)(q >> 2) * C::kWPanel;
+                        st_shared_v4(at + (uint32_t)((((q & 3) * 2) ^ (t & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(at + (uint32_t)((((q & 3) * 2 + 1) ^ (t & 7)) << 4), w[4], w[5], w[6], w[7]);
+                    }
+                } else if (!seen) {
+#pragma unroll
+                    for (int pn = 0; pn < C::kWPanels; ++pn)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) st_shared_v4(dst + pn * C::kWPanel + q * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_at(C::kWFull + j % C::kWS));
+                    if (E4) mbar_arrive(bar_at(C::kVFree + st));
+                }
+            }
+            if (!ok) *abort_flag = 1;
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         // ---------------- softmax: row r of tile x, keys 64 hf .. 64 hf + 63 of each tile of keys ----------------
         const int x = warp >> 3, hf = (warp >> 2) & 1, r = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -346,32 +414,31 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_at(C::kQFull + x));
+                if (lane == 0) mbar_arrive(bar_at(C::kGo + x));
             }
             const float qk = qs * p.scale_log2;
             const int row_lo = p.window > 0 ? imax(0, pos - p.window + 1) : 0;
             // keys that every row of the tile sees
             const int all_hi = s.kv - s.n + tok_first + 1;
             const int all_lo = p.window > 0 ? imax(0, s.kv - s.n + tok_last - p.window + 1) : 0;
-            // 16 columns lie in one page: its scales
-            const int page_shift = __ffs(imin(c.P, kTile)) - 1 - 4;
             float mref = -INFINITY, l = 0.f;   // the row's reference (the same in both threads) and this half's sum
             for (int j = 0; j < nt; ++j) {
                 const int tile0 = (first_tile + j) * kTile;
-                // rows of V that no row of the item sees must not reach the product
-                // (both tiles clear them: each before its own product)
-                if (hf == 0 && (tile0 < it.lo || tile0 + kTile > it.hi)) {
-                    ok &= wait(C::kVFull + j % C::kVS, j / C::kVS);
-                    if (tile0 + r < it.lo || tile0 + r >= it.hi) {
+                float ks[NS], lvs[NS], ivs[NS];
+                if constexpr (E4) {
+                    ok &= wait(C::kMetaBar + j % kMeta, j / kMeta);
 #pragma unroll
-                        for (int pn = 0; pn < C::kPanels; ++pn)
-#pragma unroll
-                            for (int q = 0; q < C::kPB / 16; ++q)
-                                st_shared_v4(sb + C::kOffV + (j % C::kVS) * C::kTileB + pn * C::kPanel + r * C::kPB + q * 16, 0u, 0u, 0u, 0u);
+                    for (int q = 0; q < NS; ++q) {
+                        const int box = NS > 1 ? hf * NS + q : (c.P >= kTile ? 0 : hf);
+                        const float4 sc = ld_shared_v4f(sb + C::kOffMeta + (uint32_t)((j % kMeta) * 8 + box) * 16u);
+                        ks[q] = qk * sc.x;
+                        lvs[q] = sc.y;
+                        ivs[q] = sc.z;
                     }
-                    fence_async_smem();
+                } else {
+                    ks[0] = qk;
+                    lvs[0] = 0.f;
                 }
-                if (E4) ok &= wait(C::kMetaBar + j % kMeta, j / kMeta);
                 ok &= wait(C::kSFull + x, j);
                 __syncwarp();
                 tc_fence_after();
@@ -381,28 +448,30 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 tmem_wait_ld();
                 const bool masked = tile0 < all_lo || tile0 + kTile > all_hi;
                 const int see_lo = row_lo - tile0 - hf * kCols, see_hi = pos + 1 - tile0 - hf * kCols;   // columns the row sees
+                constexpr int kGroup = kCols / NS;   // columns of one page
                 if (masked) {
 #pragma unroll
                     for (int e = 0; e < kCols; ++e) a[e] = e >= see_lo && e < see_hi ? a[e] : -INFINITY;
+                    if constexpr (E4) {
+                        // where the row sees nothing of a page, its scales may be anything
+#pragma unroll
+                        for (int q = 0; q < NS; ++q)
+                            if (!((q + 1) * kGroup > see_lo && q * kGroup < see_hi)) {
+                                ks[q] = ivs[q] = 1.f;
+                                lvs[q] = 0.f;
+                            }
+                    }
                 }
-                const uint32_t ma = sb + C::kOffMeta + (j % kMeta) * 128u;
                 float mx = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < kCols / 16; ++q) {
-                    float m0 = fmax3(a[q * 16], a[q * 16 + 1], a[q * 16 + 2]), m1 = fmax3(a[q * 16 + 3], a[q * 16 + 4], a[q * 16 + 5]);
+                for (int q = 0; q < NS; ++q) {
+                    float m0 = fmaxf(a[q * kGroup], a[q * kGroup + 1]), m1 = fmaxf(a[q * kGroup + 2], a[q * kGroup + 3]);
 #pragma unroll
-                    for (int e = 6; e < 14; e += 4) {
-                        m0 = fmax3(m0, a[q * 16 + e], a[q * 16 + e + 1]);
-                        m1 = fmax3(m1, a[q * 16 + e + 2], a[q * 16 + e + 3]);
+                    for (int e = q * kGroup + 4; e < (q + 1) * kGroup; e += 4) {
+                        m0 = fmax3(m0, a[e], a[e + 1]);
+                        m1 = fmax3(m1, a[e + 2], a[e + 3]);
                     }
-                    m0 = fmax3(m0, m1, fmaxf(a[q * 16 + 14], a[q * 16 + 15]));
-                    if (E4) {
-                        const float4 sc = ld_shared_v4f(ma + (uint32_t)((hf * 4 + q) >> page_shift) * 16u);
-                        m0 = m0 == -INFINITY ? m0 : fmaf(m0, qk * sc.x, sc.y);
-                    } else {
-                        m0 *= qk;
-                    }
-                    mx = fmaxf(mx, m0);
+                    mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ks[q], lvs[q]));
                 }
                 // the row's reference moves when a score of either half exceeds it by
                 // more than 2^8; the vote also says that both halves of S were read,
@@ -413,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     const float top = fmaxf(mx, *other);
                     float alpha = 1.f;
                     if (top - mref > 8.f) {
-                        const float up = top - C::kHead;
+                        const float up = top;
                         alpha = ex2_approx(mref - up);
                         mref = up;
                         l *= alpha;
@@ -435,24 +504,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     bar_pair(pair);   // the maxima were read
                 }
                 const float nref = mref == -INFINITY ? 0.f : mref;
-                uint32_t w1[E4 ? 8 : 16], w2[8];   // terms of 32 columns
+                uint32_t w[16];   // weights of 32 columns
 #pragma unroll
                 for (int q = 0; q < kCols / 16; ++q) {
-                    float ks = qk, add = -nref, ivs = 1.f;
-                    if (E4) {
-                        const float4 sc = ld_shared_v4f(ma + (uint32_t)((hf * 4 + q) >> page_shift) * 16u);
-                        ks = qk * sc.x;
-                        add = sc.y - nref;
-                        ivs = sc.z;
-                        // where the row sees nothing of the page, its scales may be anything
-                        if (masked && !(q * 16 + 16 > see_lo && q * 16 < see_hi)) {
-                            ks = ivs = 1.f;
-                            add = 0.f;
-                        }
-                    }
-                    const uint64_t ks2 = f2_pack(ks, ks), add2 = f2_pack(add, add);
+                    const int n = q * 16 / kGroup;
+                    const float add = lvs[n] - nref;
+                    const uint64_t ks2 = f2_pack(ks[n], ks[n]), add2 = f2_pack(add, add);
                     uint64_t sum2 = 0;
-                    uint32_t hw[8];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         float u, v;
@@ -460,34 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         u = ex2_approx(u);
                         v = ex2_approx(v);
                         sum2 = f2_add(sum2, f2_pack(u, v));
-                        hw[e / 2] = E4 ? cvt_f16x2(u, v) : pack_bf16(u, v);
+                        w[(q & 1) * 8 + e / 2] = E4 ? cvt_f16x2(u, v) : pack_bf16(u, v);
                     }
                     float s0, s1;
                     f2_unpack(sum2, s0, s1);
-                    l = E4 ? fmaf(s0 + s1, ivs, l) : l + (s0 + s1);
-                    if constexpr (E4) {
-#pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const uint32_t t = e4m3x4(hw[e], hw[e + 1]);
-                            uint32_t e0, e1;
-                            e4m3x4_to_f16x2(t, e0, e1);
-                            w1[(q & 1) * 4 + e / 2] = t;
-                            w2[(q & 1) * 4 + e / 2] = e4m3x4(rest(hw[e], e0), rest(hw[e + 1], e1));
-                        }
-                        if (q & 1) {
-                            tmem_st8(t_s + hf * 16 + (q >> 1) * 8, w1);
-                            tmem_st8(t_s + 32 + hf * 16 + (q >> 1) * 8, w2);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w1[(q & 1) * 8 + e] = hw[e];
-                        if (q & 1) tmem_st16(t_s + hf * 32 + (q >> 1) * 16, w1);
-                    }
+                    l = E4 ? fmaf(s0 + s1, ivs[n], l) : l + (s0 + s1);
+                    if (q & 1) tmem_st16(t_s + hf * 32 + (q >> 1) * 16, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_at(C::kPFull + x));
+                if (lane == 0) mbar_arrive(bar_at(C::kGo + x));
             }
             *mine = l;
             bar_pair(pair);
@@ -582,7 +623,7 @@ __global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__
     if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
 }
 
-template <bool E4, int D>
+template <bool E4, int D, int NS>
 cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st) {
     using C = Cfg<E4, D>;
     static std::atomic<bool> configured[64];
@@ -590,11 +631,11 @@ cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!configured[dev & 63].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(tile_kernel<E4, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        e = cudaFuncSetAttribute(tile_kernel<E4, D, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         configured[dev & 63].store(true, std::memory_order_release);
     }
-    e = masw_launch(tile_kernel<E4, D>, dim3(plan.items * plan.n_split, p.c.Hkv, p.c.B), dim3(kThreads), C::kSmem, st, 1, p, plan.n_split);
+    e = masw_launch(tile_kernel<E4, D, NS>, dim3(plan.items * plan.n_split, p.c.Hkv, p.c.B), dim3(kThreads), C::kSmem, st, 1, p, plan.n_split);
     if (e != cudaSuccess || plan.n_split == 1) return e;
     return masw_launch(tile_merge_kernel<D>, dim3(plan.items * 32, p.c.Hkv, p.c.B), dim3(256), 0, st, 1, p, plan.n_split, plan.items);
 }
@@ -602,8 +643,10 @@ cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t 
 }  // namespace tile
 
 cudaError_t launch_paged_tiles(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st) {
-    if (p.c.k_scale) return p.c.D == 64 ? tile::launch<true, 64>(p, plan, st) : tile::launch<true, 128>(p, plan, st);
-    return p.c.D == 64 ? tile::launch<false, 64>(p, plan, st) : tile::launch<false, 128>(p, plan, st);
+    if (!p.c.k_scale) return p.c.D == 64 ? tile::launch<false, 64, 1>(p, plan, st) : tile::launch<false, 128, 1>(p, plan, st);
+    if (p.c.P >= 64) return p.c.D == 64 ? tile::launch<true, 64, 1>(p, plan, st) : tile::launch<true, 128, 1>(p, plan, st);
+    if (p.c.P == 32) return p.c.D == 64 ? tile::launch<true, 64, 2>(p, plan, st) : tile::launch<true, 128, 2>(p, plan, st);
+    return p.c.D == 64 ? tile::launch<true, 64, 4>(p, plan, st) : tile::launch<true, 128, 4>(p, plan, st);
 }
 
 }  // namespace masw
