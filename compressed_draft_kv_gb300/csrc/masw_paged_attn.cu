@@ -12,14 +12,34 @@
 
 namespace masw {
 
-// The plan of the many-rows kernel: 128 / G tokens a tile, two tiles an item.  One
-// split, unless the items leave SMs without work: then as many as fill them once.
+// The plan of the many-rows kernel: 128 / G tokens a tile, two tiles an item, one
+// CTA an SM.  Fewer items than SMs: all are cut into as many splits as fill the SMs
+// once.  A few waves of items: those of the last, partly filled wave are cut so that
+// it ends sooner (256 items on 152 SMs: 104 of them in 7 parts each, 1.7 waves
+// instead of 2).  Many waves: nothing is cut, the end of the last one costs little.
 static TilePlan tile_plan(const PagedView& c, int max_rows, int G, int sms) {
     TilePlan t;
     const int tokens = 2 * (kTile / G);
     t.items = (max_rows + tokens - 1) / tokens;
-    const long long ctas = (long long)t.items * c.Hkv * c.B;
-    t.n_split = (int)std::max(1ll, std::min<long long>(64, sms / ctas));
+    const long long units = (long long)t.items * c.Hkv * c.B;
+    t.cut = 0;
+    t.n_split = 1;
+    if (units < sms) {
+        t.n_split = (int)std::min<long long>(64, sms / units);
+        t.cut = t.n_split > 1 ? (int)units : 0;
+    } else if (units < 6ll * sms) {
+        const int rest = (int)(units % sms);
+        double best = 0.9;
+        for (int n = 2; n <= 8; ++n) {
+            const double waves = (double)(((long long)rest * n + sms - 1) / sms) / n;
+            if (rest && waves < best - 0.01) {
+                best = waves;
+                t.n_split = n;
+                t.cut = rest;
+            }
+        }
+    }
+    t.whole = (int)(units - t.cut);
     return t;
 }
 
@@ -35,6 +55,7 @@ static int paged_attn_sizes(const PagedView& c, const char* who, int rows, int m
     if (n_q_heads < c.Hkv || n_q_heads % c.Hkv || n_q_heads / c.Hkv > 128)
         return fail("n_q_heads must be a multiple of n_kv_heads, at most 128 per kv head");
     if ((long long)rows * n_q_heads > 0x7fffffffll) return fail("rows * n_q_heads must be below 2^31");
+    if (((long long)rows * (n_q_heads / c.Hkv) / 128 + 1) * c.Hkv * c.B > 0x3fffffffll) return fail("too many rows and heads");
     *mr = ragged ? std::min(max_rows, rows) : rows / c.B;
     if ((long long)c.B * c.Hkv * (c.cap / kTile + 2) > 0x7fffffffll) return fail("batch * heads * table too large");
     return MASW_OK;
@@ -53,7 +74,7 @@ static int device_sms(int* sms) {
 static size_t workspace_bytes_for(const PagedView& c, int max_rows, int G, int sms) {
     if ((long long)max_rows * G > kRowsMax) {
         const TilePlan t = tile_plan(c, max_rows, G, sms);
-        return t.n_split == 1 ? 16 : (size_t)t.items * t.n_split * c.Hkv * c.B * 256 * (c.D + 2) * sizeof(float);
+        return t.cut == 0 ? 16 : (size_t)t.cut * t.n_split * 256 * (c.D + 2) * sizeof(float);
     }
     return (size_t)sms * 2 * kRowsMax * (c.D + 2) * sizeof(float);   // two partials a CTA
 }
@@ -107,6 +128,7 @@ extern "C" int masw_paged_attn(const masw_paged_t* cache, const int* kv_len, con
     if (((uintptr_t)q | (uintptr_t)o | (uintptr_t)workspace) & 15) return fail("q, o and workspace must be 16-byte aligned");
     if (((uintptr_t)kv_len | (uintptr_t)row_start | (uintptr_t)lse | (uintptr_t)status) & 3)
         return fail("kv_len, row_start, lse and status must be 4-byte aligned");
+    if (workspace_bytes < 16) return fail("workspace too small");
     int sms = 0;
     if ((rc = device_sms(&sms))) return rc;
     if (workspace_bytes < workspace_bytes_for(p.c, mr, n_q_heads / p.c.Hkv, sms)) return fail("workspace too small");
@@ -134,7 +156,6 @@ extern "C" int masw_paged_attn(const masw_paged_t* cache, const int* kv_len, con
         e = launch_paged_rows(p, sms, (cudaStream_t)stream);
     } else {
         const TilePlan t = tile_plan(p.c, mr, p.G, sms);
-        if ((long long)t.items * 64 > 0x7fffffffll) return fail("max_rows too large");
         e = launch_paged_tiles(p, t, (cudaStream_t)stream);
     }
     if (e != cudaSuccess) return masw_set_error(nullptr, MASW_ECUDA, std::string("paged_attn: ") + cudaGetErrorString(e));

@@ -132,10 +132,11 @@ __device__ int make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n
     return total;
 }
 
-// How the many-rows kernel cuts its work: items of 256 rows a sequence, and splits
-// of an item's keys.
+// How the many-rows kernel cuts its work: `items` of 256 rows a (sequence, kv head)
+// pair; of all pairs' items, the first `whole` take a CTA each and the last `cut`
+// are cut along the keys into n_split CTAs.
 struct TilePlan {
-    int items, n_split;
+    int items, whole, cut, n_split;
 };
 // The many-rows kernel and its merge (masw_paged_tile.cu).
 cudaError_t launch_paged_tiles(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st);

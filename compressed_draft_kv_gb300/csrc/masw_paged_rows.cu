@@ -191,6 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         *abort_flag = 0;
         fence_mbar_init();
     }
+    if (tid == 32) {
+        tma_prefetch_map(&p.tm_k);
+        tma_prefetch_map(&p.tm_v);
+    }
     pdl_wait();
     pdl_trigger();
     int* const err = p.status ? p.status : err_sink;
@@ -457,19 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             check_and_scale(nxt);
             Batch nn;
             next_batch(nn);
-            const float lvs = cur.vs == 1.f ? 0.f : __log2f(cur.vs), ivs = __frcp_rn(cur.vs);
             for (int j = 0; j < cur.nt; ++j, ++i) {
                 const int b0 = imax(cur.lo, j * bpt), b1 = imin(cur.hi, (j + 1) * bpt);   // the tile's boxes
                 if (turn > 0) ok = all(wait(freed + st, turn - 1));
                 if (!ok) break;
-                if (scales) {
-                    if (lane / bpt == j) meta[(i % kMeta) * 8 + lane % bpt] = make_float4(cur.ks, lvs, ivs, 0.f);
-                    __syncwarp();
-                }
-                if (elect_one()) {
-                    if (scales) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
-                    mbar_expect_tx(bars + full + st, (uint32_t)(imax(0, b1 - b0) * box * C::kRB));
-                }
+                if (elect_one()) mbar_expect_tx(bars + full + st, (uint32_t)(imax(0, b1 - b0) * box * C::kRB));
                 __syncwarp();
                 // the whole warp walks the boxes, one lane issues
                 for (int q = b0; q < b1; ++q) {
@@ -483,6 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     }
                 }
                 __syncwarp();
+                if (scales) {   // behind the copies, which need not wait for them
+                    if (lane / bpt == j)
+                        meta[(i % kMeta) * 8 + lane % bpt] = make_float4(cur.ks, cur.vs == 1.f ? 0.f : __log2f(cur.vs), __frcp_rn(cur.vs), 0.f);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
+                }
                 if (++st == stages) {
                     st = 0;
                     ++turn;

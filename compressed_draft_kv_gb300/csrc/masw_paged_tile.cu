@@ -20,11 +20,10 @@
 // most; the outputs are means over many of them).
 //
 // Warps 0-7 and 8-15: softmax of the two tiles; 16 issues the matrix products of
-// whichever tile is ready, all of a tile's at once: P V and the next S of one tile
-// run while the other one's softmax does (in a fixed order each tile waited behind
-// the other; with an issuing warp a tile the products of both interleaved, ended
-// together, and left the tensor cores idle during both softmaxes); 17 watches K and V
-// for it.  18: page ids,
+// the tiles in turn, all of a tile's at once: P V and the next S of one tile run
+// while the other one's softmax does (with an issuing warp a tile the products of
+// both interleaved, ended together, and left the tensor cores idle during both
+// softmaxes); 17 watches K and V for it, so that one barrier stands before a step.  18: page ids,
 // scales and K; 19: page ids and V; 20-23 widen V and clear the rows that no query
 // sees.  A long cache under few
 // rows is cut into splits, whose partial results a second kernel joins.
@@ -37,6 +36,10 @@ using namespace tc;
 
 constexpr int kThreads = 768;
 constexpr int kMeta = 8;
+// Weights may reach 2^14 (fp16 ends at 2^16; what lies 2^-38 below the largest is
+// lost): a row's reference then hardly ever moves after its first tile, and moving
+// it stalls the tile for ~2000 cycles.
+constexpr float kSlack = 14.f;
 
 template <bool E4, int D>
 struct Cfg {
@@ -49,8 +52,11 @@ struct Cfg {
     static constexpr uint32_t kSwz = kPB == 128 ? 2 : 4;
     static constexpr uint32_t kAtom = 8 * kPB;
     static constexpr int kTerms = E4 ? 2 : 1;                   // of Q
-    static constexpr int kKS = 3, kVS = 2;                      // stages of K and V
-    static constexpr int kWS = 2;                               // buffers of V as the products read it (bf16: the stages)
+    // stages of K and V (a load takes ~3000 cycles, two tiles' worth; e4m3's V stages
+    // are free once widened), and buffers of V as the products read it (bf16: the
+    // stages)
+    static constexpr int kKS = D == 64 ? 4 : 3, kVS = D == 64 ? 4 : (E4 ? 3 : 2);
+    static constexpr int kWS = E4 ? 2 : kVS;
     // V as the products read it, 2 bytes an element: panels of 64 elements
     static constexpr int kWPanels = D / 64;
     static constexpr uint32_t kWPanel = kTile * 128;
@@ -60,8 +66,8 @@ struct Cfg {
     static constexpr uint32_t kOffV = kOffK + kKS * kTileB;
     static constexpr uint32_t kOffW = E4 ? kOffV + kVS * kTileB : kOffV;
     static constexpr uint32_t kOffMeta = kOffW + kWS * kWideB;
-    static constexpr uint32_t kOffRow = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);   // a float per tile, half and row
-    static constexpr uint32_t kOffBar = kOffRow + 4 * kTile * 4;
+    static constexpr uint32_t kOffRow = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);   // a float a row
+    static constexpr uint32_t kOffBar = kOffRow + 2 * kTile * 4;
     static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kWFull = kVFree + kVS, kWFree = kWFull + kWS, kMetaBar = kWFree + kWS;
     static constexpr int kSFull = kMetaBar + (E4 ? kMeta : 0), kGo = kSFull + 2, kOFull = kGo + 2;   // kGo: all that a step of a tile needs
     static constexpr int kDone = kOFull + 2, kBars = kDone + 1;
@@ -105,9 +111,17 @@ __host__ __device__ inline Item item_of(int item, int n, int kv, int window, int
     return x;
 }
 
+// Unit `unit` of the line of all items, the last (longest) item of a pair first.
+__device__ __forceinline__ void unit_of(int unit, int items, int Hkv, int& b, int& h, int& item) {
+    const int pair = unit / items;
+    item = items - 1 - (unit - pair * items);
+    b = pair / Hkv;
+    h = pair - b * Hkv;
+}
+
 // NS: pages that half a tile of keys (64) touches, as far as scales go: 1, 2 or 4
 template <bool E4, int D, int NS>
-__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ PagedAttnParams p, int n_split) {
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ PagedAttnParams p, const TilePlan plan) {
     using C = Cfg<E4, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -120,11 +134,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     auto bar_at = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
     const PagedView& c = p.c;
     const int G = p.G, tokens = kTile / G;   // tokens of a 128-row tile
+    if (tid == 0) {
+        tma_prefetch_map(&p.tm_k);
+        tma_prefetch_map(&p.tm_v);
+    }
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.z, h = blockIdx.y, Hkv = c.Hkv;
-    const int split = (int)blockIdx.x % n_split, n_items = (int)gridDim.x / n_split;
-    const int item = n_items - 1 - (int)blockIdx.x / n_split;   // the longest first
+    // units [0, plan.whole) are whole items, the later ones are cut into splits
+    const int over = (int)blockIdx.x - plan.whole, n_split = over < 0 ? 1 : plan.n_split;
+    const int unit = over < 0 ? (int)blockIdx.x : plan.whole + over / n_split, split = over < 0 ? 0 : over % n_split;
+    int b, h, item;
+    unit_of(unit, plan.items, c.Hkv, b, h, item);
     const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
     if (!s.ok || s.n > p.max_rows || (sb & 1023u)) {
         if (tid == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
@@ -138,6 +158,20 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const int first_tile = it.t0 + j0;
     const bool two = it.tok1 - it.tok0 > tokens;                       // the second tile has rows
     int* const err = p.status ? p.status : err_sink;
+
+    // the softmax threads' row of tile x and half hf of the keys, and its Q, loaded
+    // while the block is set up
+    const int x = (warp >> 3) & 1, hf = (warp >> 2) & 1, r = tid & 127;
+    const int tok_first = it.tok0 + x * tokens;                       // of the tile
+    const int tok_last = imin(it.tok1, tok_first + tokens) - 1;
+    const int tok = imin(tok_first + r / G, tok_last), g = r % G;
+    const bool active = warp < 16 && (x == 0 || two);
+    uint4 q[D / 16];
+    if (active) {
+        const __nv_bfloat16* src = p.q + (size_t)(s.r0 + tok) * p.q_stride + (size_t)(h * G + g) * D + hf * (D / 2);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
+    }
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tslot)) : "memory");
@@ -165,53 +199,48 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 16) {
             // ---------------- matrix products ----------------
-            auto ready = [&](int bar, int phase) { return all(mbar_test(bars + bar, (uint32_t)phase & 1u)); };
-            int next[2] = {0, two ? 0 : nt + 1};   // per tile: step j is P V of tile j - 1 and S of tile j
-            uint32_t polls = 0;
-            for (int x = 0; ok && (next[0] <= nt || next[1] <= nt); x ^= 1) {
-                const int j = x ? next[1] : next[0];
-                if (j > nt) continue;
-                if (!ready(C::kGo + x, j)) {
-                    if (all(*abort_flag != 0)) ok = false;
-                    if (++polls == kWaitPolls) {
-                        atomicExch(err, MASW_ETIMEOUT);
-                        ok = false;
+            // one lane does it all: step j of tile x is P V of key tile j - 1 and S of
+            // key tile j
+            if (elect_one()) {
+                uint32_t ks = 0, ws = 0;                 // stage of K(j), buffer of V(j - 1)
+                for (int j = 0; ok && j <= nt; ++j) {
+                    const uint64_t bv = smem_desc(sb + C::kOffW + ws * C::kWideB, C::kWPanel, 1024, 2);
+                    const uint64_t bk = smem_desc(sb + C::kOffK + ks * C::kTileB, 16, C::kAtom, C::kSwz);
+                    for (int x = 0; x < (two ? 2 : 1); ++x) {
+                        if (!wait(C::kGo + x, j)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t aq = smem_desc(sb + C::kOffQ + x * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0);
+                        const uint32_t ts = tmem + C::kColS + x * 128, to = tmem + C::kColO + x * 128;
+                        if (j > 0) {
+#pragma unroll
+                            for (int kk = 0; kk < kTile / 16; ++kk)
+                                umma_bf16_ts(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, bv + (uint64_t)((kk * 2048) >> 4), C::kIdescO, j > 1 || kk > 0);
+                            umma_commit(bar_at((E4 ? C::kWFree : C::kVFree) + ws));
+                            if (j == nt) umma_commit(bar_at(C::kOFull + x));
+                        }
+                        if (j < nt) {
+#pragma unroll
+                            for (int t = 0; t < C::kTerms; ++t)
+#pragma unroll
+                                for (int kk = 0; kk < C::kRB / 32; ++kk) {
+                                    const uint64_t a = aq + (uint64_t)((t * C::kTileB + kk * 256) >> 4);
+                                    const uint64_t bb = bk + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
+                                    if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                                    else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                                }
+                            umma_commit(bar_at(C::kSFull + x));
+                            umma_commit(bar_at(C::kKFree + ks));
+                        }
                     }
-                    continue;
+                    ks = ks + 1 == C::kKS ? 0 : ks + 1;
+                    if (j > 0) ws = ws + 1 == C::kWS ? 0 : ws + 1;
                 }
-                const int ks = j % C::kKS, ws = (j - 1) % C::kWS;
-                polls = 0;
-                tc_fence_after();
-                const uint64_t aq = smem_desc(sb + C::kOffQ + x * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0);
-                const uint32_t ts = tmem + C::kColS + x * 128, to = tmem + C::kColO + x * 128;
-                if (elect_one()) {
-                    if (j > 0) {
-                        const uint64_t bv = smem_desc(sb + C::kOffW + ws * C::kWideB, C::kWPanel, 1024, 2);
-#pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            umma_bf16_ts(to, ts + kk * 8, bv + (uint64_t)((kk * 2048) >> 4), C::kIdescO, j > 1 || kk > 0);
-                        umma_commit(bar_at((E4 ? C::kWFree : C::kVFree) + ws));
-                        if (j == nt) umma_commit(bar_at(C::kOFull + x));
-                    }
-                    if (j < nt) {
-                        const uint64_t bk = smem_desc(sb + C::kOffK + ks * C::kTileB, 16, C::kAtom, C::kSwz);
-#pragma unroll
-                        for (int t = 0; t < C::kTerms; ++t)
-#pragma unroll
-                            for (int kk = 0; kk < C::kRB / 32; ++kk) {
-                                const uint64_t a = aq + (uint64_t)((t * C::kTileB + kk * 256) >> 4);
-                                const uint64_t bb = bk + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
-                                if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
-                                else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
-                            }
-                        umma_commit(bar_at(C::kSFull + x));
-                        umma_commit(bar_at(C::kKFree + ks));
-                    }
-                }
-                __syncwarp();
-                if (x) ++next[1];
-                else ++next[0];
             }
+            __syncwarp();
+            ok = all(ok);
             // nothing may arrive on a barrier after the CTA ended
             if (ok) ok = all(wait(C::kKFree + (nt - 1) % C::kKS, (nt - 1) / C::kKS)) && all(wait((E4 ? C::kWFree : C::kVFree) + (nt - 1) % C::kWS, (nt - 1) / C::kWS));
             if (!ok) {
@@ -253,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 }
                 ks = vs = 1.f;
                 if (scales && in) {
-                    ks = __ldg(c.k_scale + (size_t)pid * Hkv + h);
-                    vs = __ldg(c.v_scale + (size_t)pid * Hkv + h);
+                    ks = __ldg(c.k_scale + (size_t)pid * c.Hkv + h);
+                    vs = __ldg(c.v_scale + (size_t)pid * c.Hkv + h);
                 }
             };
             int pid, pid1, pid2, st = 0, turn = 0, issued = 0;
@@ -266,20 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             for (int base = 0; ok && base < nt; base += bt) {
                 check_and_scale(pid1, in1, ks1, vs1);
                 load_ids(base + 2 * bt, pid2, in2);
-                const float lvs = vs == 1.f ? 0.f : __log2f(vs), ivs = __frcp_rn(vs);
                 for (int j = base; j < imin(nt, base + bt); ++j) {
                     if (turn > 0) ok = all(wait(freed + st, turn - 1));
                     if (!ok) break;
                     const int q0 = (j - base) * bpt;
                     const uint32_t boxes = __ballot_sync(0xffffffffu, in) >> q0 & (bpt == 32 ? 0xffffffffu : (1u << bpt) - 1u);
-                    if (scales) {
-                        if (lane >= q0 && lane < q0 + bpt) meta[(j % kMeta) * 8 + lane - q0] = make_float4(ks, lvs, ivs, 0.f);
-                        __syncwarp();
-                    }
-                    if (elect_one()) {
-                        if (scales) mbar_arrive(bar_at(C::kMetaBar + j % kMeta));
-                        mbar_expect_tx(bars + full + st, (uint32_t)(__popc(boxes) * box * C::kRB));
-                    }
+                    if (elect_one()) mbar_expect_tx(bars + full + st, (uint32_t)(__popc(boxes) * box * C::kRB));
                     __syncwarp();
                     for (int q = 0; q < bpt; ++q) {
                         const int id = __shfl_sync(0xffffffffu, pid, q0 + q);
@@ -292,6 +313,12 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         }
                     }
                     __syncwarp();
+                    if (scales) {   // behind the copies, which need not wait for them
+                        if (lane >= q0 && lane < q0 + bpt)
+                            meta[(j % kMeta) * 8 + lane - q0] = make_float4(ks, vs == 1.f ? 0.f : __log2f(vs), __frcp_rn(vs), 0.f);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_at(C::kMetaBar + j % kMeta));
+                    }
                     ++issued;
                     if (++st == stages) {
                         st = 0;
@@ -322,19 +349,24 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     const uint32_t src = sb + C::kOffV + st * C::kTileB + t * C::kPB;
                     const int swz = D == 128 ? t & 7 : (t >> 1) & 3;
 #pragma unroll
-                    for (int q = 0; q < D / 16; ++q) {
-                        const float4 f = ld_shared_v4f(src + ((uint32_t)(q ^ swz) << 4));
-                        uint32_t w[8];
-                        e4m3x4_to_f16x2(__float_as_uint(f.x), w[0], w[1]);
-                        e4m3x4_to_f16x2(__float_as_uint(f.y), w[2], w[3]);
-                        e4m3x4_to_f16x2(__float_as_uint(f.z), w[4], w[5]);
-                        e4m3x4_to_f16x2(__float_as_uint(f.w), w[6], w[7]);
-                        if (!seen)
+                    for (int q0 = 0; q0 < D / 16; q0 += 4) {
+                        float4 f[4];   // loads first: they are not reordered with the stores
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = 0u;
-                        const uint32_t at = dst + (uint32_t)(q >> 2) * C::kWPanel;
-                        st_shared_v4(at + (uint32_t)((((q & 3) * 2) ^ (t & 7)) << 4), w[0], w[1], w[2], w[3]);
-                        st_shared_v4(at + (uint32_t)((((q & 3) * 2 + 1) ^ (t & 7)) << 4), w[4], w[5], w[6], w[7]);
+                        for (int q = 0; q < 4; ++q) f[q] = ld_shared_v4f(src + ((uint32_t)((q0 + q) ^ swz) << 4));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[8];
+                            e4m3x4_to_f16x2(__float_as_uint(f[q].x), w[0], w[1]);
+                            e4m3x4_to_f16x2(__float_as_uint(f[q].y), w[2], w[3]);
+                            e4m3x4_to_f16x2(__float_as_uint(f[q].z), w[4], w[5]);
+                            e4m3x4_to_f16x2(__float_as_uint(f[q].w), w[6], w[7]);
+                            if (!seen)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) w[e] = 0u;
+                            const uint32_t at = dst + (uint32_t)((q0 + q) >> 2) * C::kWPanel;
+                            st_shared_v4(at + (uint32_t)(((q * 2) ^ (t & 7)) << 4), w[0], w[1], w[2], w[3]);
+                            st_shared_v4(at + (uint32_t)(((q * 2 + 1) ^ (t & 7)) << 4), w[4], w[5], w[6], w[7]);
+                        }
                     }
                 } else if (!seen) {
 #pragma unroll
@@ -355,28 +387,28 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         // ---------------- softmax: row r of tile x, keys 64 hf .. 64 hf + 63 of each tile of keys ----------------
-        const int x = warp >> 3, hf = (warp >> 2) & 1, r = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + C::kColS + x * 128 + lane_off, t_o = tmem + C::kColO + x * 128 + lane_off;
         const int pair = 1 + x * 4 + (warp & 3);                          // barrier of the two warps that share 32 rows
-        float* mine = reinterpret_cast<float*>(smem + C::kOffRow) + (x * 2 + hf) * kTile + r;
-        const float* other = mine + (hf ? -kTile : kTile);
-        const int tok_first = it.tok0 + x * tokens;                       // of the tile
-        const int tok_last = imin(it.tok1, tok_first + tokens) - 1;
-        const int tok = imin(tok_first + r / G, tok_last), g = r % G;
+        float* slot = reinterpret_cast<float*>(smem + C::kOffRow) + x * kTile + r;
+        // f of both halves' values, in both threads
+        auto both = [&](float mine, auto f) {
+            if (hf) *slot = mine;
+            bar_pair(pair);
+            if (!hf) *slot = mine = f(mine, *slot);
+            bar_pair(pair);
+            if (hf) mine = *slot;
+            return mine;
+        };
         const bool live = r < (tok_last - tok_first + 1) * G;             // rows behind repeat the last token
         const int pos = s.kv - s.n + tok;
         const size_t row = (size_t)(s.r0 + tok) * p.Hq + (size_t)h * G + g;
-        if (x == 0 || two) {
+        if (active) {
             // Q: this row's half, split into its terms
             float qs = 1.f;
             {
-                const __nv_bfloat16* src = p.q + (size_t)(s.r0 + tok) * p.q_stride + (size_t)(h * G + g) * D + hf * (D / 2);
                 const uint32_t dst = sb + C::kOffQ + x * C::kTerms * C::kTileB + (uint32_t)((r >> 3) * (C::kRB / 16) * 128 + (r & 7) * 16) +
                                      (uint32_t)(hf * (C::kRB / 32) * 128);
-                uint4 q[D / 16];
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
                 if constexpr (E4) {
                     float amax = 0.f;
 #pragma unroll
@@ -386,9 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
                     }
-                    *mine = amax;
-                    bar_pair(pair);
-                    qs = pow2_scale(fmaxf(amax, *other));
+                    qs = pow2_scale(both(amax, [](float a, float b) { return fmaxf(a, b); }));
                     const float inv = 1.f / qs;
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
@@ -443,45 +473,66 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 __syncwarp();
                 tc_fence_after();
                 constexpr int kCols = kTile / 2;
-                float a[kCols];
-                tmem_ld_cols<kCols>(t_s + hf * kCols, reinterpret_cast<uint32_t*>(a));
-                tmem_wait_ld();
+                constexpr int kGroup = kCols / NS;   // columns of one page
                 const bool masked = tile0 < all_lo || tile0 + kTile > all_hi;
                 const int see_lo = row_lo - tile0 - hf * kCols, see_hi = pos + 1 - tile0 - hf * kCols;   // columns the row sees
-                constexpr int kGroup = kCols / NS;   // columns of one page
-                if (masked) {
+                if (E4 && masked) {
+                    // where the row sees nothing of a page, its scales may be anything
 #pragma unroll
-                    for (int e = 0; e < kCols; ++e) a[e] = e >= see_lo && e < see_hi ? a[e] : -INFINITY;
-                    if constexpr (E4) {
-                        // where the row sees nothing of a page, its scales may be anything
-#pragma unroll
-                        for (int q = 0; q < NS; ++q)
-                            if (!((q + 1) * kGroup > see_lo && q * kGroup < see_hi)) {
-                                ks[q] = ivs[q] = 1.f;
-                                lvs[q] = 0.f;
-                            }
-                    }
+                    for (int q = 0; q < NS; ++q)
+                        if (!((q + 1) * kGroup > see_lo && q * kGroup < see_hi)) {
+                            ks[q] = ivs[q] = 1.f;
+                            lvs[q] = 0.f;
+                        }
                 }
-                float mx = -INFINITY;
+                // Weights relative to the row's reference, which moves when a score of
+                // either half exceeds it by more than 2^kSlack: then they are computed
+                // anew (rarely, so that nobody waits for the maximum to know).
+                uint32_t w[kCols / 2];
+                float sum;
+#pragma unroll 1
+                for (;;) {
+                    float a[kCols];
+                    tmem_ld_cols<kCols>(t_s + hf * 64, reinterpret_cast<uint32_t*>(a));
+                    tmem_wait_ld();
+                    if (masked) {
 #pragma unroll
-                for (int q = 0; q < NS; ++q) {
-                    float m0 = fmaxf(a[q * kGroup], a[q * kGroup + 1]), m1 = fmaxf(a[q * kGroup + 2], a[q * kGroup + 3]);
-#pragma unroll
-                    for (int e = q * kGroup + 4; e < (q + 1) * kGroup; e += 4) {
-                        m0 = fmax3(m0, a[e], a[e + 1]);
-                        m1 = fmax3(m1, a[e + 2], a[e + 3]);
+                        for (int e = 0; e < kCols; ++e) a[e] = e >= see_lo && e < see_hi ? a[e] : -INFINITY;
                     }
-                    mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ks[q], lvs[q]));
-                }
-                // the row's reference moves when a score of either half exceeds it by
-                // more than 2^8; the vote also says that both halves of S were read,
-                // which P overwrites
-                if (bar_pair_or(pair, mx - mref > 8.f)) {
-                    *mine = mx;
-                    bar_pair(pair);
-                    const float top = fmaxf(mx, *other);
+                    const float nref = mref == -INFINITY ? 0.f : mref;
+                    float mx = -INFINITY;
+                    sum = 0.f;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) {
+                        const float add = lvs[n] - nref;
+                        const uint64_t ks2 = f2_pack(ks[n], ks[n]), add2 = f2_pack(add, add);
+                        uint64_t sum2 = 0, sum3 = 0;
+                        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                        for (int e = n * kGroup; e < (n + 1) * kGroup; e += 4) {
+                            m0 = fmax3(m0, a[e], a[e + 1]);
+                            m1 = fmax3(m1, a[e + 2], a[e + 3]);
+                            float u0, u1, u2, u3;
+                            f2_unpack(f2_fma(f2_pack(a[e], a[e + 1]), ks2, add2), u0, u1);
+                            f2_unpack(f2_fma(f2_pack(a[e + 2], a[e + 3]), ks2, add2), u2, u3);
+                            u0 = ex2_approx(u0);
+                            u1 = ex2_approx(u1);
+                            u2 = ex2_approx(u2);
+                            u3 = ex2_approx(u3);
+                            sum2 = f2_add(sum2, f2_pack(u0, u1));
+                            sum3 = f2_add(sum3, f2_pack(u2, u3));
+                            w[e / 2] = E4 ? cvt_f16x2(u0, u1) : pack_bf16(u0, u1);
+                            w[e / 2 + 1] = E4 ? cvt_f16x2(u2, u3) : pack_bf16(u2, u3);
+                        }
+                        float s0, s1;
+                        f2_unpack(f2_add(sum2, sum3), s0, s1);
+                        sum = E4 ? fmaf(s0 + s1, ivs[n], sum) : s0 + s1;
+                        mx = fmaxf(mx, fmaf(fmaxf(m0, m1), ks[n], lvs[n]));
+                    }
+                    if (!bar_pair_or(pair, mx - mref > kSlack)) break;
+                    const float top = both(mx, [](float a, float b) { return fmaxf(a, b); });
                     float alpha = 1.f;
-                    if (top - mref > 8.f) {
+                    if (top - mref > kSlack) {
                         const float up = top;
                         alpha = ex2_approx(mref - up);
                         mref = up;
@@ -501,48 +552,26 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         }
                         tmem_wait_st();
                     }
-                    bar_pair(pair);   // the maxima were read
                 }
-                const float nref = mref == -INFINITY ? 0.f : mref;
-                uint32_t w[16];   // weights of 32 columns
-#pragma unroll
-                for (int q = 0; q < kCols / 16; ++q) {
-                    const int n = q * 16 / kGroup;
-                    const float add = lvs[n] - nref;
-                    const uint64_t ks2 = f2_pack(ks[n], ks[n]), add2 = f2_pack(add, add);
-                    uint64_t sum2 = 0;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        float u, v;
-                        f2_unpack(f2_fma(f2_pack(a[q * 16 + e], a[q * 16 + e + 1]), ks2, add2), u, v);
-                        u = ex2_approx(u);
-                        v = ex2_approx(v);
-                        sum2 = f2_add(sum2, f2_pack(u, v));
-                        w[(q & 1) * 8 + e / 2] = E4 ? cvt_f16x2(u, v) : pack_bf16(u, v);
-                    }
-                    float s0, s1;
-                    f2_unpack(sum2, s0, s1);
-                    l = E4 ? fmaf(s0 + s1, ivs[n], l) : l + (s0 + s1);
-                    if (q & 1) tmem_st16(t_s + hf * 32 + (q >> 1) * 16, w);
-                }
+                l += sum;
+                // P over the half of S that this thread read
+                tmem_st16(t_s + hf * 64, *reinterpret_cast<uint32_t(*)[16]>(w));
+                tmem_st16(t_s + hf * 64 + 16, *reinterpret_cast<uint32_t(*)[16]>(w + 16));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_at(C::kGo + x));
             }
-            *mine = l;
-            bar_pair(pair);
-            l += *other;
+            l = both(l, [](float a, float b) { return a + b; });
             ok &= wait(C::kOFull + x, 0);
             __syncwarp();
             tc_fence_after();
             float* part = nullptr;
             if (n_split > 1) {
-                const size_t unit = ((size_t)(b * Hkv + h) * n_items + item) * n_split + split;
-                part = p.part + unit * 256 * (D + 2) + (size_t)(x * 128 + r) * (D + 2);
+                part = p.part + (size_t)over * 256 * (D + 2) + x * 128 + r;   // [D + 2][256 rows]
                 if (live && hf == 0) {
-                    __stcg(part + D, l == 0.f ? -INFINITY : mref);
-                    __stcg(part + D + 1, l);
+                    __stcg(part + D * 256, l == 0.f ? -INFINITY : mref);
+                    __stcg(part + (D + 1) * 256, l);
                 }
             } else if (live && hf == 0 && p.lse) {
                 p.lse[row] = l == 0.f ? -INFINITY : (mref + __log2f(l)) * 0.6931471805599453f;
@@ -554,8 +583,11 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 tmem_ld32(t_o + q, ov);
                 tmem_wait_ld();
                 if (!live) continue;
-                if (part || p.o_f32) {
-                    float* dst = part ? part + q : reinterpret_cast<float*>(p.o) + row * D + q;
+                if (part) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) __stcg(part + (q + e) * 256, __uint_as_float(ov[e]));
+                } else if (p.o_f32) {
+                    float* dst = reinterpret_cast<float*>(p.o) + row * D + q;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
                         __stcg(reinterpret_cast<float2*>(dst + e), make_float2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv));
@@ -583,44 +615,50 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
 }
 
-// Joins the splits of every row: a warp a row, D / 32 elements a lane.
+// Joins the splits of an item: thread r row r of its 256, 32 elements a CTA.
 template <int D>
-__global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__ PagedAttnParams p, int n_split, int n_items) {
+__global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__ PagedAttnParams p, const TilePlan plan) {
     const PagedView& c = p.c;
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.z, h = blockIdx.y, G = p.G, tokens = kTile / G, lane = threadIdx.x & 31;
-    const int item = (int)blockIdx.x / 32, r = ((int)blockIdx.x % 32) * 8 + (int)(threadIdx.x >> 5);   // row of the 256
+    const int G = p.G, tokens = kTile / G, n_split = plan.n_split, r = threadIdx.x;
+    const int over = blockIdx.x, d0 = (int)blockIdx.y * 32;
+    int b, h, item;
+    unit_of(plan.whole + over, plan.items, c.Hkv, b, h, item);
     const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
     if (!s.ok || s.n > p.max_rows || item * 2 * tokens >= s.n) return;
     const Item it = item_of(item, s.n, s.kv, p.window, tokens);
     const int tok = it.tok0 + (r >> 7) * tokens + (r & 127) / G;
     if ((r & 127) >= tokens * G || tok >= it.tok1) return;
     const int chunk = (it.nt + n_split - 1) / n_split;
-    constexpr int kE = D / 32;
-    float M = -INFINITY, l = 0.f, o[kE] = {};
-    const size_t unit = ((size_t)(b * c.Hkv + h) * n_items + item) * n_split;
+    float M = -INFINITY, l = 0.f, o[32] = {};
     for (int q = 0; q < n_split && q * chunk < it.nt; ++q) {
-        const float* part = p.part + (unit + q) * 256 * (D + 2) + (size_t)r * (D + 2);
-        const float m = __ldcg(part + D), pl = __ldcg(part + D + 1);
-        float v[kE];
+        const float* part = p.part + ((size_t)over * n_split + q) * 256 * (D + 2) + r;
+        const float m = __ldcg(part + D * 256), pl = __ldcg(part + (D + 1) * 256);
+        float v[32];
 #pragma unroll
-        for (int e = 0; e < kE; e += 2) {
-            const float2 f = __ldcg(reinterpret_cast<const float2*>(part + lane * kE + e));
-            v[e] = f.x;
-            v[e + 1] = f.y;
-        }
+        for (int e = 0; e < 32; ++e) v[e] = __ldcg(part + (d0 + e) * 256);
         if (m == -INFINITY) continue;
         const float nm = fmaxf(M, m), w0 = exp2f(M - nm), w1 = exp2f(m - nm);
         l = l * w0 + pl * w1;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = o[e] * w0 + v[e] * w1;
+        for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + v[e] * w1;
         M = nm;
     }
     const size_t row = (size_t)(s.r0 + tok) * p.Hq + (size_t)h * G + (r & 127) % G;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (p.o_f32) {
+        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + row * D + d0);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) store_out(p, row * D + lane * kE + e, l == 0.f ? 0.f : o[e] / l);
-    if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+    } else {
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + d0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+    }
+    if (d0 == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
 }
 
 template <bool E4, int D, int NS>
@@ -635,9 +673,9 @@ cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t 
         if (e != cudaSuccess) return e;
         configured[dev & 63].store(true, std::memory_order_release);
     }
-    e = masw_launch(tile_kernel<E4, D, NS>, dim3(plan.items * plan.n_split, p.c.Hkv, p.c.B), dim3(kThreads), C::kSmem, st, 1, p, plan.n_split);
-    if (e != cudaSuccess || plan.n_split == 1) return e;
-    return masw_launch(tile_merge_kernel<D>, dim3(plan.items * 32, p.c.Hkv, p.c.B), dim3(256), 0, st, 1, p, plan.n_split, plan.items);
+    e = masw_launch(tile_kernel<E4, D, NS>, dim3(plan.whole + plan.cut * plan.n_split), dim3(kThreads), C::kSmem, st, 1, p, plan);
+    if (e != cudaSuccess || plan.cut == 0) return e;
+    return masw_launch(tile_merge_kernel<D>, dim3(plan.cut, D / 32), dim3(256), 0, st, 1, p, plan);
 }
 
 }  // namespace tile
