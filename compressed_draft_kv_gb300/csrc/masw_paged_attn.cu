@@ -94,6 +94,18 @@ static bool make_page_map(CUtensorMap* map, const PagedView& c, const uint8_t* b
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Q [rows][Hq][D] (token stride q_stride), boxes of 128 / G tokens x G heads x 64
+// elements, swizzled
+static bool make_q_map(CUtensorMap* map, const PagedAttnParams& p) {
+    const cuuint64_t dims[3] = {(cuuint64_t)p.c.D, (cuuint64_t)p.Hq, (cuuint64_t)p.rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.c.D * 2, (cuuint64_t)p.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(kTile / p.G)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return tma_encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" int masw_paged_workspace_bytes(const masw_paged_t* cache, int rows, int max_rows, int n_q_heads, size_t* bytes) {
     if (!bytes) return masw_set_error(nullptr, MASW_EINVAL, "paged_workspace: bytes is NULL");
     PagedView c;
@@ -156,6 +168,7 @@ extern "C" int masw_paged_attn(const masw_paged_t* cache, const int* kv_len, con
         e = launch_paged_rows(p, sms, (cudaStream_t)stream);
     } else {
         const TilePlan t = tile_plan(p.c, mr, p.G, sms);
+        if (p.q_stride >= (1ll << 39) || !make_q_map(&p.tm_q, p)) return fail("cannot describe q as a TMA tensor");
         e = launch_paged_tiles(p, t, (cudaStream_t)stream);
     }
     if (e != cudaSuccess) return masw_set_error(nullptr, MASW_ECUDA, std::string("paged_attn: ") + cudaGetErrorString(e));

@@ -14,6 +14,7 @@ constexpr int kRowsMax = 32;   // query rows of a pair that the few-rows kernel 
 struct PagedAttnParams {
     CUtensorMap tm_k;         // pages as [n_pages][Hkv][P][D], boxes of one page's rows (at most 128)
     CUtensorMap tm_v;
+    CUtensorMap tm_q;         // many rows: Q as [rows][Hq][D], boxes of a tile's tokens and one kv head's heads
     PagedView c;
     const int* kv_len;
     const int* row_start;
@@ -32,16 +33,38 @@ __device__ __forceinline__ void store_out(const PagedAttnParams& p, size_t at, f
     else reinterpret_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
 }
 
-// wait_or_abort in few instructions: the kernel is large, and what stalled it most
-// was fetching instructions.  try_wait itself suspends the thread for a while.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+// A bounded wait in few instructions and registers (the kernels are large, and what
+// stalled them most was fetching instructions): barrier and abort flag by their
+// shared-memory addresses.  try_wait itself suspends the thread for a while.  One
+// wait that gives up sets the flag, and every later one returns at once.
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t at, uint32_t v) {
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint32_t abort_flag, int* status) {
     uint32_t n = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (*abort_flag) return false;
+    while (!mbar_try_wait_at(bar, parity)) {
+        if (ld_shared_u32(abort_flag)) return false;
         if (++n == kWaitPolls) {
-            *abort_flag = 1;
-            atomicExch(err, MASW_ETIMEOUT);
+            st_shared_u32(abort_flag, 1u);
+            if (status) atomicExch(status, MASW_ETIMEOUT);
             return false;
         }
     }

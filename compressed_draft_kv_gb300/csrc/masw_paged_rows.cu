@@ -159,13 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     const uint32_t sb = smem_u32(smem);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * C::kBars);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    int* err_sink = reinterpret_cast<int*>(tslot + 2);
+    const uint32_t abort_flag = sb + C::kOffBar + 8 * C::kBars + 4;
     int* pre = reinterpret_cast<int*>(smem + C::kOffSeq);
     int* s_kv = pre + MASW_MAX_BATCH + 1;
     int* s_n = s_kv + MASW_MAX_BATCH;
     int* s_r0 = s_n + MASW_MAX_BATCH;
-    float4* meta = reinterpret_cast<float4*>(smem + C::kOffMeta);   // [kMeta][8]: K scale, log2 V scale, 1 / V scale
     float* stats = reinterpret_cast<float*>(smem + C::kOffStats);
     float* qscale = reinterpret_cast<float*>(smem + C::kOffQs);
     auto bar_at = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
@@ -188,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                                           i == C::kStat || i == C::kOFree
                                       ? 4
                                       : 1);
-        *abort_flag = 0;
+        st_shared_u32(abort_flag, 0u);
         fence_mbar_init();
     }
     if (tid == 32) {
@@ -197,7 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     }
     pdl_wait();
     pdl_trigger();
-    int* const err = p.status ? p.status : err_sink;
     const int total = make_line<kThreads>(p, pre, s_kv, s_n, s_r0, blockIdx.x == 0);
     tc_fence_before();
     __syncthreads();
@@ -215,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         }
         walk.b = lo;
     }
-    auto wait = [&](int bar, int phase) { return wait_bounded(bars + bar, (uint32_t)phase & 1u, abort_flag, err); };
+    auto wait = [&](int bar, int phase) { return wait_bounded(bar_at(bar), (uint32_t)phase & 1u, abort_flag, p.status); };
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     bool ok = true;
 
@@ -256,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             ok = all(wait(C::kKFree + (i - 1) % C::kKS, (i - 1) / C::kKS)) &&
                  all(wait(C::kQFree + (piece - 1) % C::kQBufs, (piece - 1) / C::kQBufs));
         if (!ok) {   // let the matrix products in flight end before the CTA does
-            *abort_flag = 1;
+            st_shared_u32(abort_flag, 1u);
             if (elect_one()) umma_commit(bar_at(C::kDone));
             __syncwarp();
             mbar_wait(bars + C::kDone, 0, nullptr);
@@ -401,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         // nothing may arrive on a barrier after the CTA ended
         if (ok && i > 0) ok = all(wait(C::kVFree + (i - 1) % C::kVS, (i - 1) / C::kVS));
         if (!ok) {
-            *abort_flag = 1;
+            st_shared_u32(abort_flag, 1u);
             cp_async_wait<0>();
             if (elect_one()) umma_commit(bar_at(C::kDone + 1));
             __syncwarp();
@@ -443,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         };
         auto check_and_scale = [&](Batch& x) {
             if (x.in && (x.pid < 0 || x.pid >= c.n_pages)) {
-                atomicExch(err, MASW_EINVAL);
+                if (p.status) atomicExch(p.status, MASW_EINVAL);
                 x.pid = 0;
             }
             x.ks = x.vs = 1.f;
@@ -465,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 const int b0 = imax(cur.lo, j * bpt), b1 = imin(cur.hi, (j + 1) * bpt);   // the tile's boxes
                 if (turn > 0) ok = all(wait(freed + st, turn - 1));
                 if (!ok) break;
-                if (elect_one()) mbar_expect_tx(bars + full + st, (uint32_t)(imax(0, b1 - b0) * box * C::kRB));
+                if (elect_one()) mbar_expect_tx_at(bar_at(full + st), (uint32_t)(imax(0, b1 - b0) * box * C::kRB));
                 __syncwarp();
                 // the whole warp walks the boxes, one lane issues
                 for (int q = b0; q < b1; ++q) {
@@ -481,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 __syncwarp();
                 if (scales) {   // behind the copies, which need not wait for them
                     if (lane / bpt == j)
-                        meta[(i % kMeta) * 8 + lane % bpt] = make_float4(cur.ks, cur.vs == 1.f ? 0.f : __log2f(cur.vs), __frcp_rn(cur.vs), 0.f);
+                        st_shared_v4(sb + C::kOffMeta + (uint32_t)((i % kMeta) * 8 + lane % bpt) * 16u, __float_as_uint(cur.ks),
+                                     __float_as_uint(cur.vs == 1.f ? 0.f : __log2f(cur.vs)), __float_as_uint(__frcp_rn(cur.vs)), 0u);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
                 }
@@ -494,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             nxt = nn;
         }
         // after a wait gave up, and at the end: no copy may be in flight when the CTA ends
-        if (!ok) *abort_flag = 1;
+        if (!ok) st_shared_u32(abort_flag, 1u);
         for (int k = imax(0, i - stages); k < i; ++k)
             mbar_wait(bars + full + k % stages, (uint32_t)(k / stages) & 1u, nullptr);
         __syncwarp();
@@ -542,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 float ks = qs, lvs = 0.f, ivs = 1.f;
                 if (E4) {
                     ok &= wait(C::kMetaBar + i % kMeta, i / kMeta);
-                    const float4 mt = meta[(i % kMeta) * 8 + (c.P >= kTile ? 0 : wt / c.P)];
+                    const float4 mt = ld_shared_v4f(sb + C::kOffMeta + (uint32_t)((i % kMeta) * 8 + (c.P >= kTile ? 0 : wt / c.P)) * 16u);
                     ks *= mt.x;
                     lvs = mt.y;
                     ivs = mt.z;
@@ -798,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             first = false;
             ++piece;
         }
-        if (!ok) *abort_flag = 1;
+        if (!ok) st_shared_u32(abort_flag, 1u);
     }
     tc_fence_before();
     __syncthreads();

@@ -61,16 +61,19 @@ struct Cfg {
     static constexpr int kWPanels = D / 64;
     static constexpr uint32_t kWPanel = kTile * 128;
     static constexpr uint32_t kWideB = kWPanels * kWPanel;
-    static constexpr uint32_t kOffQ = 0;                        // [2 tiles][terms]
+    static constexpr uint32_t kOffQ = 0;                        // [2 tiles][terms]; bf16: panels of 64 elements
     static constexpr uint32_t kOffK = kOffQ + 2 * kTerms * kTileB;
     static constexpr uint32_t kOffV = kOffK + kKS * kTileB;
     static constexpr uint32_t kOffW = E4 ? kOffV + kVS * kTileB : kOffV;
+    // e4m3: the bf16 rows of Q land where V will be widened
+    static constexpr uint32_t kOffLand = E4 ? kOffW : kOffQ;
     static constexpr uint32_t kOffMeta = kOffW + kWS * kWideB;
     static constexpr uint32_t kOffRow = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);   // a float a row
     static constexpr uint32_t kOffBar = kOffRow + 2 * kTile * 4;
     static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kWFull = kVFree + kVS, kWFree = kWFull + kWS, kMetaBar = kWFree + kWS;
     static constexpr int kSFull = kMetaBar + (E4 ? kMeta : 0), kGo = kSFull + 2, kOFull = kGo + 2;   // kGo: all that a step of a tile needs
-    static constexpr int kDone = kOFull + 2, kBars = kDone + 1;
+    static constexpr int kQLand = kOFull + 2;
+    static constexpr int kDone = kQLand + 1, kBars = kDone + 1;
     static constexpr uint32_t kSmem = kOffBar + 8 * kBars + 16;
     static constexpr uint32_t kColS = 0, kColO = 256;           // per tile 128 columns of S (or P) and of O
     static constexpr uint32_t kType = E4 ? 0 : 1;
@@ -128,15 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     const uint32_t sb = smem_u32(smem);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 8 * C::kBars);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    int* err_sink = reinterpret_cast<int*>(tslot + 2);
-    float4* meta = reinterpret_cast<float4*>(smem + C::kOffMeta);
+    const uint32_t abort_flag = sb + C::kOffBar + 8 * C::kBars + 4;
     auto bar_at = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
     const PagedView& c = p.c;
     const int G = p.G, tokens = kTile / G;   // tokens of a 128-row tile
-    if (tid == 0) {
+    if (tid == 32) {
+        tma_prefetch_map(&p.tm_q);
         tma_prefetch_map(&p.tm_k);
         tma_prefetch_map(&p.tm_v);
+        st_shared_u32(abort_flag, 0u);
     }
     pdl_wait();
     pdl_trigger();
@@ -146,32 +149,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     int b, h, item;
     unit_of(unit, plan.items, c.Hkv, b, h, item);
     const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
-    if (!s.ok || s.n > p.max_rows || (sb & 1023u)) {
-        if (tid == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
-        return;
-    }
-    if (item * 2 * tokens >= s.n) return;
+    const bool bad = !s.ok || s.n > p.max_rows || (sb & 1023u);
+    if (bad && tid == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
     const Item it = item_of(item, s.n, s.kv, p.window, tokens);
     const int chunk = (it.nt + n_split - 1) / n_split;
     const int j0 = split * chunk, nt = imin(it.nt, j0 + chunk) - j0;   // this CTA's tiles
-    if (nt < 1) return;                                                // the merge knows
+    if (bad || item * 2 * tokens >= s.n || nt < 1) {                   // nothing to do (the merge knows of empty splits)
+        return;
+    }
     const int first_tile = it.t0 + j0;
     const bool two = it.tok1 - it.tok0 > tokens;                       // the second tile has rows
-    int* const err = p.status ? p.status : err_sink;
-
-    // the softmax threads' row of tile x and half hf of the keys, and its Q, loaded
-    // while the block is set up
-    const int x = (warp >> 3) & 1, hf = (warp >> 2) & 1, r = tid & 127;
-    const int tok_first = it.tok0 + x * tokens;                       // of the tile
-    const int tok_last = imin(it.tok1, tok_first + tokens) - 1;
-    const int tok = imin(tok_first + r / G, tok_last), g = r % G;
-    const bool active = warp < 16 && (x == 0 || two);
-    uint4 q[D / 16];
-    if (active) {
-        const __nv_bfloat16* src = p.q + (size_t)(s.r0 + tok) * p.q_stride + (size_t)(h * G + g) * D + hf * (D / 2);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src) + k);
-    }
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tslot)) : "memory");
@@ -183,14 +170,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                                 : (i >= C::kWFull && i < C::kWFree) || (E4 && i >= C::kVFree && i < C::kWFull)    ? 4
                                 : two && ((i >= C::kKFree && i < C::kVFull) || (i >= C::kVFree && i < C::kMetaBar)) ? 2
                                                                                                                     : 1);
-        *abort_flag = 0;
         fence_mbar_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    auto wait = [&](int bar, int phase) { return wait_bounded(bars + bar, (uint32_t)phase & 1u, abort_flag, err); };
+    auto wait = [&](int bar, int phase) { return wait_bounded(bar_at(bar), (uint32_t)phase & 1u, abort_flag, p.status); };
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     bool ok = true;
 
@@ -212,7 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t aq = smem_desc(sb + C::kOffQ + x * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0);
+                        const uint64_t aq = E4 ? smem_desc(sb + C::kOffQ + x * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0)
+                                               : smem_desc(sb + C::kOffQ + x * C::kTileB, 16, 1024, 2);
                         const uint32_t ts = tmem + C::kColS + x * 128, to = tmem + C::kColO + x * 128;
                         if (j > 0) {
 #pragma unroll
@@ -226,8 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                             for (int t = 0; t < C::kTerms; ++t)
 #pragma unroll
                                 for (int kk = 0; kk < C::kRB / 32; ++kk) {
-                                    const uint64_t a = aq + (uint64_t)((t * C::kTileB + kk * 256) >> 4);
-                                    const uint64_t bb = bk + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
+                                    const uint32_t panel = (kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32;
+                                    const uint64_t a = aq + (uint64_t)((E4 ? t * C::kTileB + kk * 256 : panel) >> 4);
+                                    const uint64_t bb = bk + (uint64_t)(panel >> 4);
                                     if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
                                     else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
                                 }
@@ -244,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             // nothing may arrive on a barrier after the CTA ended
             if (ok) ok = all(wait(C::kKFree + (nt - 1) % C::kKS, (nt - 1) / C::kKS)) && all(wait((E4 ? C::kWFree : C::kVFree) + (nt - 1) % C::kWS, (nt - 1) / C::kWS));
             if (!ok) {
-                *abort_flag = 1;
+                st_shared_u32(abort_flag, 1u);
                 if (elect_one()) umma_commit(bar_at(C::kDone));
                 __syncwarp();
                 mbar_wait(bars + C::kDone, 0, nullptr);
@@ -252,6 +240,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         } else if (warp == 17) {
             // ---------------- K and V there: the ninth arrival on a step's barrier ----------------
             // (a test takes ~100 cycles: the issuing warp is left with one a step)
+            if (elect_one()) {
+                // Q: 128 / G tokens x G heads a tile (rows behind the sequence's are not
+                // used, behind all rows they read as zeros)
+                const int tiles = two ? 2 : 1;
+                mbar_expect_tx_at(bar_at(C::kQLand), (uint32_t)(tiles * tokens * G * D * 2));
+                for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                    for (int pn = 0; pn < D / 64; ++pn)
+                        tma_load_3d(sb + C::kOffLand + t * (C::kWPanels * C::kWPanel) + pn * C::kWPanel, &p.tm_q, pn * 64, h * G,
+                                    s.r0 + it.tok0 + t * tokens, bar_at(C::kQLand));
+            }
+            __syncwarp();
+            ok = all(wait(C::kQLand, 0));
             for (int j = 0; ok && j <= nt; ++j) {
                 if (j < nt) ok = all(wait(C::kKFull + j % C::kKS, j / C::kKS));
                 if (j > 0) ok = ok && all(wait(C::kWFull + (j - 1) % C::kWS, (j - 1) / C::kWS));
@@ -260,7 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     if (ok && lane == 0) mbar_arrive(bar_at(C::kGo + x));
                 }
             }
-            if (!ok) *abort_flag = 1;
+            if (!ok) {
+                st_shared_u32(abort_flag, 1u);
+                mbar_wait(bars + C::kQLand, 0, nullptr);   // no copy may be in flight when the CTA ends
+            }
         } else if (warp < 20) {
             // ---------------- page ids, scales, TMA: warp 18 K, warp 19 V ----------------
             const bool is_v = warp == 19;
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             };
             auto check_and_scale = [&](int& pid, bool in, float& ks, float& vs) {
                 if (in && (pid < 0 || pid >= c.n_pages)) {
-                    atomicExch(err, MASW_EINVAL);
+                    if (p.status) atomicExch(p.status, MASW_EINVAL);
                     pid = 0;
                 }
                 ks = vs = 1.f;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     if (!ok) break;
                     const int q0 = (j - base) * bpt;
                     const uint32_t boxes = __ballot_sync(0xffffffffu, in) >> q0 & (bpt == 32 ? 0xffffffffu : (1u << bpt) - 1u);
-                    if (elect_one()) mbar_expect_tx(bars + full + st, (uint32_t)(__popc(boxes) * box * C::kRB));
+                    if (elect_one()) mbar_expect_tx_at(bar_at(full + st), (uint32_t)(__popc(boxes) * box * C::kRB));
                     __syncwarp();
                     for (int q = 0; q < bpt; ++q) {
                         const int id = __shfl_sync(0xffffffffu, pid, q0 + q);
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     __syncwarp();
                     if (scales) {   // behind the copies, which need not wait for them
                         if (lane >= q0 && lane < q0 + bpt)
-                            meta[(j % kMeta) * 8 + lane - q0] = make_float4(ks, vs == 1.f ? 0.f : __log2f(vs), __frcp_rn(vs), 0.f);
+                            st_shared_v4(sb + C::kOffMeta + (uint32_t)((j % kMeta) * 8 + lane - q0) * 16u, __float_as_uint(ks), __float_as_uint(vs == 1.f ? 0.f : __log2f(vs)), __float_as_uint(__frcp_rn(vs)), 0u);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar_at(C::kMetaBar + j % kMeta));
                     }
@@ -332,12 +336,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 pid1 = pid2;
                 in1 = in2;
             }
-            if (!ok) *abort_flag = 1;
+            if (!ok) st_shared_u32(abort_flag, 1u);
             for (int k = imax(0, issued - stages); k < issued; ++k)
                 mbar_wait(bars + full + k % stages, (uint32_t)(k / stages) & 1u, nullptr);
         } else {
             // ---------------- V as the products read it: thread t row t of the tile ----------------
             const int t = tid & 127;
+            if (E4) ok = all(wait(C::kGo, 0)) && (!two || all(wait(C::kGo + 1, 0)));   // Q was read from where V goes
             for (int j = 0; ok && j < nt; ++j) {
                 const int key = (first_tile + j) * kTile + t, st = j % C::kVS;
                 const bool seen = key >= it.lo && key < it.hi;   // by some row; a row that none sees must not reach the product
@@ -381,12 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     if (E4) mbar_arrive(bar_at(C::kVFree + st));
                 }
             }
-            if (!ok) *abort_flag = 1;
+            if (!ok) st_shared_u32(abort_flag, 1u);
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         // ---------------- softmax: row r of tile x, keys 64 hf .. 64 hf + 63 of each tile of keys ----------------
+        const int x = warp >> 3, hf = (warp >> 2) & 1, r = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + C::kColS + x * 128 + lane_off, t_o = tmem + C::kColO + x * 128 + lane_off;
         const int pair = 1 + x * 4 + (warp & 3);                          // barrier of the two warps that share 32 rows
@@ -400,52 +406,59 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             if (hf) mine = *slot;
             return mine;
         };
+        const int tok_first = it.tok0 + x * tokens;                       // of the tile
+        const int tok_last = imin(it.tok1, tok_first + tokens) - 1;
+        const int tok = imin(tok_first + r / G, tok_last), g = r % G;
         const bool live = r < (tok_last - tok_first + 1) * G;             // rows behind repeat the last token
         const int pos = s.kv - s.n + tok;
         const size_t row = (size_t)(s.r0 + tok) * p.Hq + (size_t)h * G + g;
-        if (active) {
+        if (x == 0 || two) {
             // Q: this row's half, split into its terms
             float qs = 1.f;
-            {
+            if constexpr (E4) {
+                ok = wait(C::kQLand, 0);
+                const uint32_t src = sb + C::kOffLand + x * (C::kWPanels * C::kWPanel) + (D == 128 ? hf * C::kWPanel : 0) + r * 128;
                 const uint32_t dst = sb + C::kOffQ + x * C::kTerms * C::kTileB + (uint32_t)((r >> 3) * (C::kRB / 16) * 128 + (r & 7) * 16) +
                                      (uint32_t)(hf * (C::kRB / 32) * 128);
-                if constexpr (E4) {
-                    float amax = 0.f;
+                auto chunk_of = [&](int k) {   // eight elements
+                    const int ch = D == 128 ? k : hf * 4 + k;
+                    return ld_shared_v4f(src + ((uint32_t)(ch ^ (r & 7)) << 4));
+                };
+                float amax = 0.f;
+#pragma unroll 2
+                for (int k = 0; k < D / 16; ++k) {
+                    const float4 v = chunk_of(k);
+                    float f[8];
+                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        float f[8];
-                        Elem<__nv_bfloat16>::unpack(q[k], f);
+                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
+                }
+                qs = pow2_scale(both(amax, [](float a, float b) { return fmaxf(a, b); }));
+                const float inv = 1.f / qs;
+#pragma unroll 2
+                for (int k = 0; k < D / 16; ++k) {
+                    const float4 v = chunk_of(k);
+                    float f[8];
+                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
+                    uint32_t w1[2], w2[2];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
+                    for (int e = 0; e < 2; ++e) {
+                        const float f0 = f[4 * e] * inv, f1 = f[4 * e + 1] * inv, f2 = f[4 * e + 2] * inv, f3 = f[4 * e + 3] * inv;
+                        const uint32_t a = e4m3x2(f0, f1), bq = e4m3x2(f2, f3);
+                        float d0, d1, d2, d3;
+                        f16x2_to_f32(e4m3x2_to_f16x2(a), d0, d1);
+                        f16x2_to_f32(e4m3x2_to_f16x2(bq), d2, d3);
+                        w1[e] = a | (bq << 16);
+                        w2[e] = e4m3x2(f0 - d0, f1 - d1) | (e4m3x2(f2 - d2, f3 - d3) << 16);
                     }
-                    qs = pow2_scale(both(amax, [](float a, float b) { return fmaxf(a, b); }));
-                    const float inv = 1.f / qs;
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t w1[4], w2[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4& v = q[2 * k + e / 2];
-                            const uint32_t lo = e & 1 ? v.z : v.x, hi = e & 1 ? v.w : v.y;
-                            const float f[4] = {bf16lo(lo) * inv, bf16hi(lo) * inv, bf16lo(hi) * inv, bf16hi(hi) * inv};
-                            const uint32_t a = e4m3x2(f[0], f[1]), bq = e4m3x2(f[2], f[3]);
-                            float d0, d1, d2, d3;
-                            f16x2_to_f32(e4m3x2_to_f16x2(a), d0, d1);
-                            f16x2_to_f32(e4m3x2_to_f16x2(bq), d2, d3);
-                            w1[e] = a | (bq << 16);
-                            w2[e] = e4m3x2(f[0] - d0, f[1] - d1) | (e4m3x2(f[2] - d2, f[3] - d3) << 16);
-                        }
-                        st_shared_v4(dst + k * 128, w1[0], w1[1], w1[2], w1[3]);
-                        st_shared_v4(dst + C::kTileB + k * 128, w2[0], w2[1], w2[2], w2[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) st_shared_v4(dst + k * 128, q[k].x, q[k].y, q[k].z, q[k].w);
+                    const uint32_t at = dst + (uint32_t)((k >> 1) * 128 + (k & 1) * 8);
+                    st_shared_v2(at, w1[0], w1[1]);
+                    st_shared_v2(at + C::kTileB, w2[0], w2[1]);
                 }
                 fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_at(C::kGo + x));
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_at(C::kGo + x));
             const float qk = qs * p.scale_log2;
             const int row_lo = p.window > 0 ? imax(0, pos - p.window + 1) : 0;
             // keys that every row of the tile sees
@@ -604,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 }
             }
             tc_fence_before();
-            if (!ok) *abort_flag = 1;
+            if (!ok) st_shared_u32(abort_flag, 1u);
         }
     }
     tc_fence_before();
