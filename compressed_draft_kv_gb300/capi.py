@@ -318,7 +318,10 @@ def masw_paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> masw_paged
                      MASW_E4M3 if e4 else MASW_BF16, n, p, h, d, B,
                      page_table.stride(0) if B > 1 else page_table.shape[1])
     c.tensors = tensors
+    # what the calls below need on every step, looked up once
+    c.address = ctypes.addressof(c)
     c.device, c.bf16, c.int32, c.f32 = k.device, torch.bfloat16, torch.int32, torch.float32
+    c.cuda_index = k.device.index if k.device.type == "cuda" else None
     return c
 
 
@@ -329,23 +332,36 @@ def masw_rope(cos_sin, interleaved=False) -> masw_rope_t:
         raise ValueError("cos_sin must be contiguous fp32 [n_pos, rot_dim]")
     r = masw_rope_t(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved))
     r.tensors = [cos_sin]
+    r.address = ctypes.addressof(r)
     return r
 
 
 def _token_rows(name, x, heads, dim, cache):
     """Token stride of x [rows, heads, dim] (bf16 on the cache's device; heads and elements dense)."""
-    if x.dtype != cache.bf16 or x.device != cache.device or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or x.dtype is not cache.bf16 or x.device != cache.device:
         raise ValueError(f"{name} must be bfloat16 [rows, {heads}, {dim}] on the cache's device")
-    st = x.stride()
     if st[2] != 1 or (st[1] != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return st[0] if x.shape[0] > 1 else 0
+    return st[0] if shape[0] > 1 else 0
 
 
 def _ints(name, x, n, cache):
-    if x is not None and (x.dtype != cache.int32 or x.device != cache.device or x.numel() < n or not x.is_contiguous()):
+    if x is None:
+        return None
+    if x.dtype is not cache.int32 or x.numel() < n or x.device != cache.device or not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 with at least {n} elements on the cache's device")
-    return _ptr(x)
+    return x.data_ptr()
+
+
+def _cache_stream(stream, cache):
+    """The stream to launch on, as a handle; the cache's device has to be the current one."""
+    if cache.cuda_index is None:
+        return stream or 0
+    import torch
+    if torch.cuda.current_device() != cache.cuda_index:
+        raise ValueError("the cache lies on another device than the current one")
+    return torch._C._cuda_getCurrentRawStream(cache.cuda_index) if stream is None else stream
 
 
 def masw_paged_append(cache, kv_len, k, v, rope=None, pos=None, q=None, q_out=None, row_start=None, status=None,
@@ -353,26 +369,27 @@ def masw_paged_append(cache, kv_len, k, v, rope=None, pos=None, q=None, q_out=No
     """Append the K/V rows [rows, Hkv, D] of new tokens to a paged cache, K (and q -> q_out [rows, Hq, D]) rotated by
     `rope` on the way.  kv_len [batch] counts them already; row_start [batch + 1] says whose rows are whose (None:
     rows / batch each).  k, v and q may be slices of a fused projection.  status: optional int32 word."""
-    rows, (B, H, D) = k.shape[0], (cache.batch, cache.n_kv_heads, cache.head_dim)
+    rows, B, H, D = k.shape[0], cache.batch, cache.n_kv_heads, cache.head_dim
     ks, vs = _token_rows("k", k, H, D, cache), _token_rows("v", v, H, D, cache)
     hq = qs = 0
+    q_ptr = q_out_ptr = None
     if q is not None:
         hq = q.shape[1]
         qs = _token_rows("q", q, hq, D, cache)
-        if q_out is None or q_out.dtype != q.dtype or q_out.shape != q.shape or not q_out.is_contiguous():
+        if q_out is None or q_out.dtype is not cache.bf16 or q_out.shape != q.shape or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous bfloat16 of q's shape")
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
     if v.shape[0] != rows or (q is not None and q.shape[0] != rows):
         raise ValueError("k, v and q differ in rows")
-    _check(load().masw_paged_append(ctypes.byref(cache), _ints("kv_len", kv_len, B, cache),
-                                    _ints("row_start", row_start, B + 1, cache), rows, _ptr(k), _ptr(v), ks, vs,
-                                    None if rope is None else ctypes.byref(rope), _ints("pos", pos, rows, cache),
-                                    _ptr(q), _ptr(q_out), hq, qs, _ints("status", status, 1, cache),
-                                    _device_stream(stream, cache)))
+    _check(load().masw_paged_append(cache.address, _ints("kv_len", kv_len, B, cache), _ints("row_start", row_start, B + 1, cache),
+                                    rows, k.data_ptr(), v.data_ptr(), ks, vs, None if rope is None else rope.address,
+                                    _ints("pos", pos, rows, cache), q_ptr, q_out_ptr, hq, qs,
+                                    _ints("status", status, 1, cache), _cache_stream(stream, cache)))
 
 
 def masw_paged_workspace_bytes(cache, rows, max_rows, n_q_heads) -> int:
     out = ctypes.c_size_t()
-    _check(load().masw_paged_workspace_bytes(ctypes.byref(cache), rows, max_rows, n_q_heads, ctypes.byref(out)))
+    _check(load().masw_paged_workspace_bytes(cache.address, rows, max_rows, n_q_heads, ctypes.byref(out)))
     return out.value
 
 
@@ -381,31 +398,25 @@ def masw_paged_attn(cache, kv_len, q, o, lse=None, row_start=None, max_rows=None
     """Causal attention of q [rows, Hq, D] bf16 over a paged cache -> o [rows, Hq, D] (bf16 or fp32), lse [rows, Hq]
     fp32.  With row_start, max_rows bounds the rows of one sequence (None: all of them).  Without a workspace (uint8,
     masw_paged_workspace_bytes), one is allocated."""
-    rows, hq, D = q.shape
+    rows, hq, _ = q.shape
     B = cache.batch
     qs = _token_rows("q", q, hq, cache.head_dim, cache)
-    if o.shape != q.shape or not o.is_contiguous() or o.device != cache.device or o.dtype not in (cache.bf16, cache.f32):
+    if o.shape != q.shape or not o.is_contiguous() or o.device != cache.device or (o.dtype is not cache.bf16 and o.dtype is not cache.f32):
         raise ValueError("o must be contiguous bfloat16 or float32 of q's shape")
-    if lse is not None and (tuple(lse.shape) != (rows, hq) or lse.dtype != cache.f32 or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous float32 [rows, Hq]")
-    mr = rows if max_rows is None else max_rows
-    if row_start is None:
-        mr = rows // B
+    lse_ptr = None
+    if lse is not None:
+        if lse.shape != (rows, hq) or lse.dtype is not cache.f32 or not lse.is_contiguous() or lse.device != cache.device:
+            raise ValueError("lse must be contiguous float32 [rows, Hq]")
+        lse_ptr = lse.data_ptr()
+    mr = rows // B if row_start is None else (rows if max_rows is None else max_rows)
     if workspace is None:
         import torch
         workspace = torch.empty(masw_paged_workspace_bytes(cache, rows, mr, hq), dtype=torch.uint8, device=cache.device)
-    _check(load().masw_paged_attn(ctypes.byref(cache), _ints("kv_len", kv_len, B, cache),
-                                  _ints("row_start", row_start, B + 1, cache), rows, mr, _ptr(q), hq, qs, window, scale,
-                                  _ptr(o), MASW_BF16 if o.dtype == cache.bf16 else MASW_F32, _ptr(lse),
-                                  _ints("status", status, 1, cache), _ptr(workspace), workspace.numel(),
-                                  _device_stream(stream, cache)))
-
-
-def _device_stream(stream, cache):
-    import torch
-    if torch.cuda.is_available() and cache.device.type == "cuda" and cache.device.index != torch.cuda.current_device():
-        raise ValueError("the cache lies on another device than the current one")
-    return _stream(stream)
+    _check(load().masw_paged_attn(cache.address, _ints("kv_len", kv_len, B, cache), _ints("row_start", row_start, B + 1, cache),
+                                  rows, mr, q.data_ptr(), hq, qs, window, scale, o.data_ptr(),
+                                  MASW_BF16 if o.dtype is cache.bf16 else MASW_F32, lse_ptr,
+                                  _ints("status", status, 1, cache), workspace.data_ptr(), workspace.nbytes,
+                                  _cache_stream(stream, cache)))
 
 
 # ---------------------------------------------------------------- plumbing --

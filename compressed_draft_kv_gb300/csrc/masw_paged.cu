@@ -2,20 +2,19 @@
 // and values join the target's cache) with the rotary rotation of K and Q on the
 // way, and the argument checks of the paged-cache calls.
 //
-// One CTA works on one (sequence, touched page) unit and up to 256 / (D / 16)
-// heads of K, V and Q.  D / 16 lanes own one head: they walk the page's new rows
-// twice, first for the largest magnitude (e4m3 pages: the page's scale must
-// cover them all before one is stored), then to store.  A (page, head) belongs
-// to one group of lanes, so its scale needs no atomics and the result does not
-// depend on timing.  Bound by HBM for prompts (bf16 rows in, pages out), by the
-// chain of dependent loads (row range, length, page id, old scale, rows) for a
-// decode step.
+// Work is cut into units of one touched page of one sequence.  A (page, head)
+// belongs to one group of threads, so its scale needs no atomics and the result
+// does not depend on timing.  Two kernels: in the one for steps a few lanes own
+// a head and walk the unit's few rows; in the one for many rows a CTA holds all
+// rows of a (page, head) at once.
 #include "masw_paged.cuh"
 
 #include <algorithm>
 #include <cstring>
 
 namespace masw {
+
+constexpr int kStages = 3;   // heads on their way to shared memory, in the kernel for many rows, and the one at work
 
 struct PagedAppendParams {
     PagedView c;
@@ -30,6 +29,7 @@ struct PagedAppendParams {
     const int* pos;
     int n_pos, rot, interleaved;
     int rows, Hq;
+    int per_seq;   // units of every sequence, or 0: rows differ, append_unit_base
     int* status;
 };
 
@@ -47,34 +47,42 @@ __host__ __device__ inline LaneChunks lane_chunks(int t, int rot, int interleave
     return LaneChunks{8 * t, rot / 2 + 8 * t, 8 * t};
 }
 
+// The rotation of a lane's sixteen elements by o = eight cosines, eight sines:
+// element i of the first chunk with element i of the second, or adjacent ones
+// within each chunk (then rot0 and rot1 say whether a chunk is rotated).  Each
+// product and sum is rounded once (no fused multiply-add), so the stored values
+// are those of the written formula.
+__device__ __forceinline__ void rotate16(float (&x)[16], const float (&o)[16], int interleaved, bool rot0, bool rot1) {
+    auto turn = [](float& a, float& b, float c, float s) {
+        const float a0 = a, b0 = b;
+        a = __fsub_rn(__fmul_rn(a0, c), __fmul_rn(b0, s));
+        b = __fadd_rn(__fmul_rn(b0, c), __fmul_rn(a0, s));
+    };
+    if (interleaved) {
+        if (rot0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], o[i], o[8 + i]);
+        if (rot1)
+#pragma unroll
+            for (int i = 4; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], o[i], o[8 + i]);
+    } else if (rot0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(x[i], x[i + 8], o[i], o[8 + i]);
+    }
+}
+
 __device__ __forceinline__ void load_rotated(const __nv_bfloat16* src, const LaneChunks& lc, bool rotate, const float* cs,
                                              int rot, int interleaved, float (&x)[16]) {
     Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(src + lc.c0), x);
     Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(src + lc.c1), x + 8);
     if (!rotate || lc.ang < 0) return;
-    float c[8], s[8];
+    float o[16];
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
-        *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + lc.ang + i);
-        *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(cs + rot / 2 + lc.ang + i);
+        *reinterpret_cast<float4*>(o + i) = *reinterpret_cast<const float4*>(cs + lc.ang + i);
+        *reinterpret_cast<float4*>(o + 8 + i) = *reinterpret_cast<const float4*>(cs + rot / 2 + lc.ang + i);
     }
-    // each product and sum rounded once (no fused multiply-add), so the stored
-    // values are those of the written formula
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = x[i], b = x[i + 8];
-            x[i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-            x[i + 8] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-        }
-    }
+    rotate16(x, o, interleaved, true, true);
 }
 
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const LaneChunks& lc, const float (&x)[16]) {
@@ -90,112 +98,297 @@ __device__ int find_sequence(const PagedAppendParams& p, int u) {
     for (int i0 = 0; i0 < p.c.B; i0 += blockDim.x) {
         const int i = i0 + threadIdx.x;
         int r0 = 0;
-        if (i < p.c.B) r0 = p.row_start ? p.row_start[i] : i * (p.rows / p.c.B);
+        if (i < p.c.B) r0 = p.row_start[i];
         found += __syncthreads_count(i < p.c.B && append_unit_base(imax(0, r0), i, p.c.P) <= u);
     }
     return imax(0, found - 1);
 }
 
-__global__ void __launch_bounds__(256) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
+// one CTA checks every sequence's row range and length
+__device__ __forceinline__ void check_sequences(const PagedAppendParams& p) {
+    if (p.status && blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < p.c.B; i += blockDim.x) {
+            const SeqRows s = seq_rows(p.row_start, p.kv_len, i, p.rows, p.c.B, p.c.cap);
+            if (!s.ok || s.n > s.kv) atomicExch(p.status, MASW_EINVAL);
+        }
+}
+
+// the page and the rows of unit `u`
+struct AppendUnit {
+    int ra, rb;      // positions of the unit's rows: [ra, rb)
+    int row0;        // row of position 0 (row = row0 + position)
+    int off;         // slots of the page before ra
+    int pid;         // the page, if `placed`
+    bool placed;     // the table names a page of the pool
+};
+__device__ __forceinline__ bool find_unit(const PagedAppendParams& p, int u, AppendUnit& w) {
+    const PagedView& c = p.c;
+    const int b = p.per_seq ? u / p.per_seq : find_sequence(p, u);
+    const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
+    if (s.n < 1 || s.n > s.kv) return false;
+    const int p0 = s.kv - s.n, lp = p.per_seq ? u % p.per_seq : u - append_unit_base(s.r0, b, c.P), page = p0 / c.P + lp;
+    if (lp < 0 || page > (s.kv - 1) / c.P) return false;
+    w.ra = imax(p0, page * c.P);
+    w.rb = imin(s.kv, (page + 1) * c.P);
+    w.row0 = s.r0 - p0;
+    w.off = w.ra - page * c.P;
+    w.pid = c.table[(size_t)b * c.table_stride + page];
+    w.placed = w.pid >= 0 && w.pid < c.n_pages;
+    if (!w.placed && threadIdx.x == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
+    return true;
+}
+
+// the scale of a page that holds `off` rows at scale `old` and gets rows of
+// largest magnitude amax
+__device__ __forceinline__ float joined_scale(float amax, float old, int off) {
+    const float sc = pow2_scale(amax);
+    return off > 0 ? (amax > 0.f ? fmaxf(sc, old) : old) : sc;
+}
+// sixteen stored values times f (old scale / new scale), rounded again
+__device__ __forceinline__ void rescale16(uint8_t* at, float f) {
+    uint4 w = *reinterpret_cast<uint4*>(at);
+    uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a0, a1, a2, a3;
+        f16x2_to_f32(e4m3x2_to_f16x2(wp[i] & 0xffffu), a0, a1);
+        f16x2_to_f32(e4m3x2_to_f16x2(wp[i] >> 16), a2, a3);
+        wp[i] = e4m3x2(a0 * f, a1 * f) | (e4m3x2(a2 * f, a3 * f) << 16);
+    }
+    *reinterpret_cast<uint4*>(at) = w;
+}
+// x / sc as e4m3.  A power of two (every scale this file makes; a pool filled
+// elsewhere may hold others) divides exactly by a multiplication.
+__device__ __forceinline__ void store_e4m3(uint8_t* dst, const LaneChunks& lc, const float (&x)[16], float sc) {
+    const uint32_t bits = __float_as_uint(sc);
+    uint32_t w[4];
+    if ((bits & 0x807fffffu) == 0u && bits >= 0x00800000u && bits <= 0x7e000000u) {
+        const float f = __uint_as_float(0x7f000000u - bits);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = e4m3x2(x[4 * i] * f, x[4 * i + 1] * f) | (e4m3x2(x[4 * i + 2] * f, x[4 * i + 3] * f) << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = e4m3x2(x[4 * i] / sc, x[4 * i + 1] / sc) | (e4m3x2(x[4 * i + 2] / sc, x[4 * i + 3] / sc) << 16);
+    }
+    *reinterpret_cast<uint2*>(dst + lc.c0) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(dst + lc.c1) = make_uint2(w[2], w[3]);
+}
+
+// Few rows a unit.  R rows of a head at a time, D / 16 lanes each, walk the page's
+// new rows twice, first for the largest magnitude (e4m3 pages: the page's scale
+// must cover them all before one is stored), then to store; a lane's first row stays in
+// its registers between the two.  Bound by the chain of dependent loads: row
+// range, length, page id, rows and old scale.  One row of 8 sequences takes 3.3 us, 6
+// rows of 32 sequences 4.6 us (bf16 pages), most of it the launch and that chain.
+template <int R>
+__global__ void __launch_bounds__(256, 3) paged_append_step_kernel(const __grid_constant__ PagedAppendParams p) {
     pdl_wait();
     pdl_trigger();
     const PagedView& c = p.c;
-    const int tid = threadIdx.x, P = c.P;
-    // one CTA checks every sequence's row range and length
-    if (p.status && blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = tid; i < c.B; i += blockDim.x) {
-            const SeqRows s = seq_rows(p.row_start, p.kv_len, i, p.rows, c.B, c.cap);
-            if (!s.ok || s.n > s.kv) atomicExch(p.status, MASW_EINVAL);
-        }
-    const int u = blockIdx.x, b = find_sequence(p, u);
-    const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
-    if (s.n < 1 || s.n > s.kv) return;
-    const int p0 = s.kv - s.n, lp = u - append_unit_base(s.r0, b, P);
-    const int page = p0 / P + lp;
-    if (lp < 0 || page > (s.kv - 1) / P) return;
-    const int ra = imax(p0, page * P), rb = imin(s.kv, (page + 1) * P);   // positions of this unit's rows
-    const int pid = c.table[(size_t)b * c.table_stride + page];
-    const bool placed = pid >= 0 && pid < c.n_pages;
-    if (!placed && tid == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
+    check_sequences(p);
+    AppendUnit w;
+    if (!find_unit(p, blockIdx.x, w)) return;
 
-    const int L = c.D / 16, t = tid % L, heads = 2 * c.Hkv + (p.q ? p.Hq : 0);
-    const int hh = (int)blockIdx.y * ((int)blockDim.x / L) + tid / L;
+    const int tid = threadIdx.x, P = c.P;
+    const int L = c.D / 16, t = tid % L, sub = tid / L % R, heads = 2 * c.Hkv + (p.q ? p.Hq : 0);
+    const int hh = (int)blockIdx.y * ((int)blockDim.x / (L * R)) + tid / (L * R);
     const bool is_q = hh >= 2 * c.Hkv, is_v = !is_q && hh >= c.Hkv;
-    const bool live = hh < heads && (is_q || placed);
+    const bool live = hh < heads && (is_q || w.placed), quant = live && !is_q && c.k_scale;
     const int h = is_q ? hh - 2 * c.Hkv : (is_v ? hh - c.Hkv : hh);
     const __nv_bfloat16* src = is_q ? p.q : (is_v ? p.v : p.k);
     const long long stride = is_q ? p.q_stride : (is_v ? p.v_stride : p.k_stride);
     const bool rotate = p.cos_sin != nullptr && !is_v;
     const LaneChunks lc = lane_chunks(t, rotate ? p.rot : 0, p.interleaved);
     auto load = [&](int pos, float (&x)[16]) {
-        const int row = s.r0 + pos - p0;
+        const int row = w.row0 + pos;
         const int rp = p.pos ? p.pos[row] : pos;
         const bool in = rp >= 0 && rp < p.n_pos;
         if (rotate && !in && t == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
         load_rotated(src + (size_t)row * stride + (size_t)h * c.D, lc, rotate && in, p.cos_sin + (size_t)(in ? rp : 0) * p.rot,
                      p.rot, p.interleaved, x);
     };
-    float x[16];
-    if (is_q) {
-        if (live)
-            for (int pos = ra; pos < rb; ++pos) {
-                load(pos, x);
-                store_bf16(p.q_out + ((size_t)(s.r0 + pos - p0) * p.Hq + h) * c.D, lc, x);
-            }
-    } else if (!c.k_scale) {
-        if (live)
-            for (int pos = ra; pos < rb; ++pos) {
-                load(pos, x);
-                uint8_t* page0 = (is_v ? c.v : c.k) + (size_t)pid * c.page_bytes;
-                store_bf16(reinterpret_cast<__nv_bfloat16*>(page0) + ((size_t)h * P + pos % P) * c.D, lc, x);
-            }
-    }
+    uint8_t* base = (is_v ? c.v : c.k) + (size_t)w.pid * c.page_bytes;
+    float* sp = (is_v ? c.v_scale : c.k_scale) + (size_t)w.pid * c.Hkv + h;
+    const int first = live ? w.ra + sub : w.rb;
+    float x0[16], x[16], old = 0.f, amax = 0.f;
+    if (quant && w.off > 0) old = *sp;
+    if (first < w.rb) load(first, x0);
+    if (live && !quant)
+        for (int pos = first; pos < w.rb; pos += R) {
+            if (pos > first) load(pos, x0);
+            store_bf16(is_q ? p.q_out + ((size_t)(w.row0 + pos) * p.Hq + h) * c.D
+                            : reinterpret_cast<__nv_bfloat16*>(base) + ((size_t)h * P + pos % P) * c.D,
+                       lc, x0);
+        }
     if (!c.k_scale) return;
-    float amax = 0.f;
-    if (live && !is_q)
-        for (int pos = ra; pos < rb; ++pos) {
+    if (quant && first < w.rb) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x0[i]));
+        for (int pos = first + R; pos < w.rb; pos += R) {
             load(pos, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x[i]));
         }
-    for (int o = 1; o < L; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (!live || is_q) return;
-    float* sp = (is_v ? c.v_scale : c.k_scale) + (size_t)pid * c.Hkv + h;
-    uint8_t* base = (is_v ? c.v : c.k) + (size_t)pid * c.page_bytes + (size_t)h * P * c.D;
-    const int off = ra - page * P;
-    float sc = pow2_scale(amax);
-    if (off > 0) {
-        const float old = *sp;
-        sc = amax > 0.f ? fmaxf(sc, old) : old;
-        if (sc > old) {
-            // rows already there are rounded again to the larger scale
-            const float f = old / sc;
-            for (int r = 0; r < off; ++r) {
-                uint4* rp = reinterpret_cast<uint4*>(base + (size_t)r * c.D) + t;
-                uint4 w = *rp;
-                uint32_t* wp = reinterpret_cast<uint32_t*>(&w);
+    }
+    for (int o = 1; o < L * R; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __syncwarp();   // the old scale is read by every lane before one replaces it
+    if (!quant) return;
+    base += (size_t)h * P * c.D;
+    const float sc = joined_scale(amax, old, w.off);
+    if (w.off > 0 && sc > old)
+        for (int r = sub; r < w.off; r += R) rescale16(base + (size_t)r * c.D + 16 * t, old / sc);
+    for (int pos = first; pos < w.rb; pos += R) {
+        if (pos > first) load(pos, x0);
+        store_e4m3(base + (size_t)(pos % P) * c.D, lc, x0, sc);
+    }
+    if (t == 0 && sub == 0) *sp = sc;
+}
+
+// Many rows a unit.  A CTA of P D / (16 NP) threads holds a whole (page, head) in
+// fp32 registers, NP rows a thread: one read, the largest magnitude over the
+// CTA, one write.  It does `hg` heads one after the other, the next ones' rows on their
+// way to shared memory (kStages: 2 119 us, 3 112, 4 113), and keeps the cosines and
+// sines of its rows for all of them; reading them again for every head costs
+// 186 us.  P D = 32768 leaves no registers for that (NP = 4).  Bound by HBM: a 32K
+// prompt of 24 + 2 * 8 heads of 128 into e4m3 pages of 64 tokens takes 112 us,
+// 5.5 TB/s; walking the rows with the other kernel's loop took 268.
+template <int NP>
+__global__ void __launch_bounds__(512) paged_append_page_kernel(const __grid_constant__ PagedAppendParams p, int hg) {
+    __shared__ uint32_t s_max[2][16];
+    extern __shared__ __align__(16) uint8_t smem[];
+    pdl_wait();
+    pdl_trigger();
+    const PagedView& c = p.c;
+    check_sequences(p);
+    AppendUnit w;
+    if (!find_unit(p, blockIdx.x, w)) return;
+
+    constexpr bool kHold = NP <= 2;
+    const int tid = threadIdx.x, P = c.P, D = c.D;
+    const int L = D / 16, t = tid % L, G = (int)blockDim.x / L;
+    const int heads = 2 * c.Hkv + (p.q ? p.Hq : 0);
+    const int h0 = (int)blockIdx.y * hg, h1 = imin(h0 + hg, heads);
+    const bool rope = p.cos_sin != nullptr, any_rot = rope && (h0 < c.Hkv || h1 > 2 * c.Hkv);
+    // chunks of eight elements: the pairs of a lane lie in its two chunks, or (adjacent
+    // pairs, rows that are not rotated) within each of them
+    const LaneChunks plain{8 * t, D / 2 + 8 * t, -1};
+    const LaneChunks turned = rope && !p.interleaved ? lane_chunks(t, p.rot, 0) : plain;
+    const bool rot0 = rope && turned.c0 < p.rot, rot1 = rope && turned.c1 < p.rot;
+    const int a0 = p.interleaved ? turned.c0 / 2 : turned.ang, a1 = p.interleaved ? turned.c1 / 2 : turned.ang + 4;
+
+    int row[NP];
+    bool has[NP], in[NP];
+    const float* angles[NP];
+    float cs[kHold ? NP : 1][16];
+    auto load_angles = [&](const float* at, float (&o)[16]) {
+        if (rot0) {
+            *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(at + a0);
+            *reinterpret_cast<float4*>(o + 8) = *reinterpret_cast<const float4*>(at + p.rot / 2 + a0);
+        }
+        if (rot1) {
+            *reinterpret_cast<float4*>(o + 4) = *reinterpret_cast<const float4*>(at + a1);
+            *reinterpret_cast<float4*>(o + 12) = *reinterpret_cast<const float4*>(at + p.rot / 2 + a1);
+        }
+    };
+    // this thread's part of a head on its way: stage, row and chunk; no thread reads another's
+    auto slot = [&](int stage, int j, int i) { return (unsigned)((((stage * NP + j) * 2 + i) * (int)blockDim.x + tid) * 16); };
+    auto fetch = [&](int hh, int stage) {
+        const bool q = hh >= 2 * c.Hkv, v = !q && hh >= c.Hkv;
+        const __nv_bfloat16* src = q ? p.q + (size_t)(hh - 2 * c.Hkv) * D : (v ? p.v + (size_t)(hh - c.Hkv) * D : p.k + (size_t)hh * D);
+        const long long stride = q ? p.q_stride : (v ? p.v_stride : p.k_stride);
+        const LaneChunks& lc = v ? plain : turned;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float a0, a1, a2, a3;
-                    f16x2_to_f32(e4m3x2_to_f16x2(wp[i] & 0xffffu), a0, a1);
-                    f16x2_to_f32(e4m3x2_to_f16x2(wp[i] >> 16), a2, a3);
-                    wp[i] = e4m3x2(a0 * f, a1 * f) | (e4m3x2(a2 * f, a3 * f) << 16);
-                }
-                *rp = w;
+        for (int j = 0; j < NP; ++j) {
+            const __nv_bfloat16* at = src + (size_t)row[j] * stride;
+            cp_async16(smem_u32(smem) + slot(stage, j, 0), at + lc.c0, has[j] ? 16 : 0);
+            cp_async16(smem_u32(smem) + slot(stage, j, 1), at + lc.c1, has[j] ? 16 : 0);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        const int pos = w.ra + j * G + tid / L;
+        has[j] = pos < w.rb;
+        row[j] = w.row0 + (has[j] ? pos : w.ra);
+    }
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (h0 + i < h1) fetch(h0 + i, i);
+        cp_async_commit();
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        in[j] = false;
+        angles[j] = nullptr;
+        if (any_rot && has[j]) {
+            const int rp = p.pos ? p.pos[row[j]] : row[j] - w.row0;
+            in[j] = rp >= 0 && rp < p.n_pos;
+            if (!in[j] && t == 0 && p.status) atomicExch(p.status, MASW_EINVAL);
+            if (in[j]) {
+                angles[j] = p.cos_sin + (size_t)rp * p.rot;
+                if (kHold) load_angles(angles[j], cs[kHold ? j : 0]);
             }
         }
     }
-    for (int pos = ra; pos < rb; ++pos) {
-        load(pos, x);
-        uint8_t* dst = base + (size_t)(pos % P) * c.D;
-        uint32_t w[4];
+    int par = 0, stage = 0;
+    for (int hh = h0; hh < h1; ++hh) {
+        const bool is_q = hh >= 2 * c.Hkv, is_v = !is_q && hh >= c.Hkv;
+        const int h = is_q ? hh - 2 * c.Hkv : (is_v ? hh - c.Hkv : hh);
+        const LaneChunks lc = is_v ? plain : turned;
+        cp_async_wait<kStages - 2>();
+        float x[NP][16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = e4m3x2(x[4 * i] / sc, x[4 * i + 1] / sc) | (e4m3x2(x[4 * i + 2] / sc, x[4 * i + 3] / sc) << 16);
-        *reinterpret_cast<uint2*>(dst + lc.c0) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2*>(dst + lc.c1) = make_uint2(w[2], w[3]);
+        for (int j = 0; j < NP; ++j) {
+            Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(smem + slot(stage, j, 0)), x[j]);
+            Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(smem + slot(stage, j, 1)), x[j] + 8);
+        }
+        if (hh + kStages - 1 < h1) fetch(hh + kStages - 1, stage > 0 ? stage - 1 : kStages - 1);
+        cp_async_commit();
+        stage = stage + 1 < kStages ? stage + 1 : 0;
+        if (!is_v)
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                if (in[j]) {
+                    float(&o)[16] = cs[kHold ? j : 0];
+                    if (!kHold) load_angles(angles[j], o);
+                    rotate16(x[j], o, p.interleaved, rot0, rot1);
+                }
+        if (is_q || !c.k_scale) {
+            if (is_q || w.placed)
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+                    if (has[j]) {
+                        __nv_bfloat16* dst =
+                            is_q ? p.q_out + ((size_t)row[j] * p.Hq + h) * D
+                                 : reinterpret_cast<__nv_bfloat16*>((is_v ? c.v : c.k) + (size_t)w.pid * c.page_bytes) +
+                                       ((size_t)h * P + w.off + j * G + tid / L) * D;
+                        store_bf16(dst, lc, x[j]);
+                    }
+            continue;
+        }
+        if (!w.placed) continue;
+        float* sp = (is_v ? c.v_scale : c.k_scale) + (size_t)w.pid * c.Hkv + h;
+        uint8_t* base = (is_v ? c.v : c.k) + (size_t)w.pid * c.page_bytes + (size_t)h * P * D;
+        const float old = w.off > 0 ? *sp : 0.f;   // read by all before the barrier, written behind it
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x[j][i]));
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+        if (tid % 32 == 0) s_max[par][tid / 32] = top;
+        __syncthreads();
+        uint32_t all = 0;
+        for (int i = 0; i < (int)blockDim.x / 32; ++i) all = max(all, s_max[par][i]);
+        par ^= 1;
+        const float sc = joined_scale(__uint_as_float(all), old, w.off);
+        if (w.off > 0 && sc > old)
+            for (int r = tid / L; r < w.off; r += G) rescale16(base + (size_t)r * D + 16 * t, old / sc);
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+            if (has[j]) store_e4m3(base + (size_t)(w.off + j * G + tid / L) * D, lc, x[j], sc);
+        if (tid == 0) *sp = sc;
     }
-    if (t == 0) *sp = sc;
 }
 
 }  // namespace masw
@@ -291,10 +484,37 @@ extern "C" int masw_paged_append(const masw_paged_t* cache, const int* kv_len, c
     p.v = (const __nv_bfloat16*)v;
     p.rows = rows;
     p.status = status;
-    const int per_cta = 256 / (p.c.D / 16), heads = 2 * p.c.Hkv + p.Hq;
-    const int gy = (heads + per_cta - 1) / per_cta;
-    const cudaError_t e = masw_launch(paged_append_kernel, dim3(append_units(rows, p.c.B, p.c.P), gy), dim3(256), 0,
-                                      (cudaStream_t)stream, 1, p);
+    const int heads = 2 * p.c.Hkv + p.Hq, per = rows / p.c.B;
+    // n rows touch at most (n - 2) / P + 2 pages, one row one
+    if (!row_start) p.per_seq = per > 1 ? (per - 2) / p.c.P + 2 : 1;
+    const int units = row_start ? append_units(rows, p.c.B, p.c.P) : p.c.B * p.per_seq;
+    cudaError_t e;
+    // Many rows a page pay for a CTA that holds whole pages.  Its time hardly depends
+    // on the rows, the other kernel's grows with them: 32 sequences, 64-token pages,
+    // 40 heads of 128: 10.5 us at 4 rows and 11.0 at 12, against 4.5 and 7.7 (then 0.5 us
+    // for every 4 rows).  When its CTAs fit at once, it wins earlier (8 sequences: 5.5 us
+    // against 5.0 at 8 rows and 6.1 at 12; one: 3.1 against 3.3 at 1 row).
+    const long long page_rows = (long long)p.c.B * p.c.P;
+    if (rows * 3ll >= 2 * page_rows || (rows * 8ll >= page_rows && (long long)units * heads <= 768)) {
+        const int lanes = p.c.P * p.c.D / 16, np = lanes > 1024 ? 4 : 2;
+        // heads one CTA does in turn: up to 16, while two rounds of CTAs remain (a 32K prompt:
+        // 4 heads 146 us, 8 heads 135, 16 heads 130, before rows went through shared memory)
+        int hg = 1;
+        while (hg < 16 && (long long)units * ((heads + 2 * hg - 1) / (2 * hg)) * (lanes / np) >= 152ll * 2048) hg *= 2;
+        const size_t smem = (size_t)lanes * 32 * kStages;
+        auto kern = np == 2 ? paged_append_page_kernel<2> : paged_append_page_kernel<4>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(32 * 2048 * kStages));
+        if (e == cudaSuccess)
+            e = masw_launch(kern, dim3(units, (heads + hg - 1) / hg), dim3(lanes / np), smem, (cudaStream_t)stream, 1, p, hg);
+    } else {
+        // Rows of a head side by side shorten the walk: 8 sequences of 4 rows 3.7 us against
+        // 6.3.  They take four times the CTAs, too many at 256 sequences of fewer than 8 rows
+        // (2 rows: 14.0 us against 9.5; 8 rows: 21 against 24).
+        auto ctas_y = [&](int r) { return (heads * (p.c.D / 16) * r + 255) / 256; };
+        const bool wide = per > 1 && (per >= 8 || (long long)units * ctas_y(4) <= 1024);
+        e = masw_launch(wide ? paged_append_step_kernel<4> : paged_append_step_kernel<1>, dim3(units, ctas_y(wide ? 4 : 1)),
+                        dim3(256), 0, (cudaStream_t)stream, 1, p);
+    }
     if (e != cudaSuccess) return masw_set_error(nullptr, MASW_ECUDA, std::string("paged_append: ") + cudaGetErrorString(e));
     return MASW_OK;
 }

@@ -156,6 +156,67 @@ def test_append_reports_bad_lengths_rows_pages_and_positions_and_skips_them():
             assert np.array_equal(got["k"], want["k"]) and np.array_equal(got["v_scale"], want["v_scale"]), what
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,page,rot,inter", [(128, 256, 128, False), (64, 128, 32, True), (128, 128, None, False)])
+def test_append_few_rows_on_large_pages(dtype, d, page, rot, inter):
+    """Steps: pages far from full, page borders inside the rows, more rows than one pass over them holds."""
+    n = [1, 5, 0, 4, 2, 9]
+    kv = [7, page + 2, 3, page, 2 * page + 1, 2 * page + 8]
+    c = Cache(kv, 3, d, page, dtype, seed=d + page + 1)
+    run_append(c, kv, n, 5, seed=11, rot=rot, inter=inter, strided=True)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 6])
+def test_append_uniform_steps_on_large_pages(rows):
+    kv = [20, 257, 256, 6, 130]
+    c = Cache(kv, 2, 128, 256, "e4m3", seed=12)
+    run_append(c, kv, [rows] * 5, 3, seed=13, rot=128, uniform=True, strided=True)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 9])
+def test_append_of_a_large_batch(rows):
+    kv = [rows + (37 * b) % 60 for b in range(300)]
+    c = Cache(kv, 4, 64, 64, "e4m3", seed=14)
+    run_append(c, kv, [rows] * 300, 8, seed=15, rot=64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page,hkv,hq", [(128, 7, 57), (256, 5, 33)])
+def test_append_of_a_prompt_with_many_heads(dtype, page, hkv, hq):
+    """A CTA takes several heads in turn, K, V and Q among them; the last group is not full."""
+    n, kv = [2500, 1301], [2507, 1301]
+    c = Cache(kv, hkv, 128, page, dtype, seed=16)
+    run_append(c, kv, n, hq, seed=17, rot=96, strided=True, n_pos=4096)
+
+
+@pytest.mark.parametrize("page", [128, 256])
+def test_append_steps_report_what_is_bad_and_skip_it(page):
+    kv, n = [20, 10, 33], [4, 2, 3]
+    for what in ("page", "length", "short", "rows", "position"):
+        c = Cache(kv, 1, 64, page, "e4m3", seed=18)
+        table, kvl, rs, pos = c.table.clone(), list(kv), starts(n), list(range(9))
+        if what == "page":
+            table[1, 0] = c.k.shape[0]
+        elif what == "length":
+            kvl[1] = table.shape[1] * page + 1
+        elif what == "short":
+            kvl[1] = 1
+        elif what == "rows":
+            rs[3] = 10
+        else:
+            pos[5] = 64
+        cc = capi.masw_paged_cache(c.k, c.v, table.to(DEV), c.ks, c.vs)
+        k, v = bf16(9, 1, 64, seed=19), bf16(9, 1, 64, seed=20)
+        before, status = c.mirror(), torch.zeros(1, dtype=torch.int32, device=DEV)
+        rope = capi.masw_rope(tables(64, 64).to(DEV))
+        capi.masw_paged_append(cc, ints(kvl), k, v, rope=rope, pos=ints(pos), row_start=ints(rs), status=status)
+        torch.cuda.synchronize()
+        assert status.item() == capi.MASW_EINVAL
+        after, hit = c.mirror(), int(c.table[2 if what == "rows" else 1, 0])
+        changed = {p for name in before for p in np.argwhere(after[name] != before[name])[:, 0].tolist()}
+        assert changed == {int(c.table[b, 0]) for b in range(3)} - (set() if what == "position" else {hit})
+
+
 def test_append_in_place_q_and_no_q():
     c = Cache([5, 40], 2, 128, 16, "bf16", seed=11)
     k, v, q = bf16(5, 2, 128), bf16(5, 2, 128, seed=1), bf16(5, 4, 128, seed=2)
