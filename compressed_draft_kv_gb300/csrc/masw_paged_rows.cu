@@ -562,6 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     }
                     // a V row that no row sees must not reach the product
                     const int st = i % C::kVS;
+                    // A wait tells a phase only from its neighbours, so the stage's tile before
+                    // has to have landed: with four stages it has (this group's last but one
+                    // product is done), with fewer once the group's last one is.
+                    if (C::kVS < 4 && turn > 0) ok &= wait(C::kPFree + group, turn - 1);
                     ok &= wait(C::kVFull + st, i / C::kVS);
                     if (!seen) {
 #pragma unroll

@@ -365,6 +365,20 @@ def test_v_scales_of_very_different_size_and_not_powers_of_two(n):
     run_attention(c, [700], n, 8, seed=10)
 
 
+@pytest.mark.parametrize("d,dtype", KINDS)
+@pytest.mark.parametrize("n,hkv,g,page,window", [(1, 8, 4, 16, 0), (6, 8, 4, 64, 0), (1, 2, 8, 32, 1000)])
+def test_a_serving_batch_repeats_bit_for_bit(d, dtype, n, hkv, g, page, window):
+    """Every SM streams several sequences one behind the other, the values' stream behind the keys'."""
+    kv = [700 + (911 * b) % 2900 for b in range(32)]
+    c = Cache(kv, hkv, d, page, dtype, seed=60)
+    o, lse = run_attention(c, kv, [n] * 32, hkv * g, seed=61, window=window, uniform=True)
+    q = bf16(32 * n, hkv * g, d, seed=61)
+    for _ in range(20):
+        o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+        capi.masw_paged_attn(c.c, ints(kv), q, o2, lse2, window=window)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_many_sequences_split_and_whole(dtype):
     """Short sequences beside long ones, one kv head: some are cut over many CTAs, some share one."""
