@@ -55,10 +55,14 @@ __host__ __device__ inline int pow2_scale_exp(uint32_t amax_bits) {
 // tiles form one line, sequence by sequence and head by head, and CTA c of C
 // takes tiles [first_tile(c), first_tile(c + 1)) of it: every CTA gets the same
 // number of tiles (give or take one; CTAs behind the last tile get none) whatever
-// the lengths are.  A pair that is
-// cut leaves one partial result for each CTA that holds a piece of it: in that
+// the lengths are.  A pair that is cut leaves one partial result for each CTA that holds a piece of it: in that
 // CTA's slot 0 if the piece is the CTA's first, else in its slot 1 (its last).
+// Where a CTA has few tiles anyway, a second piece (its Q, the first maxima, the end's
+// sums and outputs: ~3.5 us) costs more than uneven shares: then every pair gets
+// pair_ctas CTAs of its own, and CTA pair * pair_ctas + i takes tiles
+// [part_first(i), part_first(i + 1)) of the pair, possibly none, and uses slot 0.
 constexpr int kTile = 128;
+constexpr int kUneven = 3;   // tiles that a CTA may have beyond the even share
 struct TileRange {
     int lo, hi;   // visible keys of the sequence's rows: [lo, hi)
     int t0, nt;   // first tile and number of tiles (at least one: it writes the outputs)
@@ -80,6 +84,15 @@ __host__ __device__ inline int first_tile(int c, int total, int C) {
 __host__ __device__ inline int tile_owner(int t, int total, int C) {
     const int q = total / C, rem = total - q * C;
     return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q;
+}
+
+// CTAs of every pair, or 0: the line is cut evenly.  longest: tiles of the longest pair
+__host__ __device__ inline int pair_ctas(int pairs, int longest, int total, int C) {
+    const int s = pairs <= C ? C / pairs : 0;
+    return s > 0 && (longest + s - 1) / s <= total / C + kUneven ? s : 0;
+}
+__host__ __device__ inline int part_first(int i, int nt, int s) {
+    return nt > s ? (int)((long long)i * nt / s) : (i < nt ? i : nt);   // the first min(nt, s) parts have tiles
 }
 
 #ifdef __CUDACC__

@@ -104,14 +104,17 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t v, uint32_t& h0, uint32
         : "r"(v));
 }
 // The line of all pairs' tiles: pre[b] = tiles before sequence b, pre[B] = all
-// of them (returned), and the sequences' rows and lengths, by the whole CTA of NT
+// of them, and the sequences' rows and lengths, by the whole CTA of NT
 // threads.  A sequence whose rows or length are not possible has no tiles.
+struct Line {
+    int total, longest;      // tiles of all pairs, and of the longest
+};
 template <int NT>
-__device__ int make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n, int* s_r0, bool report) {
+__device__ Line make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n, int* s_r0, bool report) {
     constexpr int kPer = (MASW_MAX_BATCH + NT - 1) / NT;
-    __shared__ int warp_sum[NT / 32];
+    __shared__ int warp_sum[NT / 32], warp_top[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, B = p.c.B;
-    int mine[kPer], sum = 0;
+    int mine[kPer], sum = 0, top = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int b = tid * kPer + k;
@@ -125,7 +128,9 @@ __device__ int make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n
             s_kv[b] = s.kv;
             s_n[b] = s.n;
             s_r0[b] = s.r0;
-            mine[k] = tile_range(s.n, s.kv, p.window).nt * p.c.Hkv;
+            const int nt = tile_range(s.n, s.kv, p.window).nt;
+            mine[k] = nt * p.c.Hkv;
+            top = imax(top, nt);
         }
         sum += mine[k];
     }
@@ -135,13 +140,18 @@ __device__ int make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n
         const int up = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= o) scan += up;
     }
-    if (lane == 31) warp_sum[tid >> 5] = scan;
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 31) {
+        warp_sum[tid >> 5] = scan;
+        warp_top[tid >> 5] = top;
+    }
     __syncthreads();
-    int before = 0, total = 0;
+    int before = 0, total = 0, longest = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
         if (w < tid >> 5) before += warp_sum[w];
         total += warp_sum[w];
+        longest = imax(longest, warp_top[w]);
     }
     before += scan - sum;
 #pragma unroll
@@ -152,7 +162,7 @@ __device__ int make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_n
     }
     if (tid == 0) pre[B] = total;
     __syncthreads();
-    return total;
+    return Line{total, longest};
 }
 
 // How the many-rows kernel cuts its work: `items` of 256 rows a (sequence, kv head)

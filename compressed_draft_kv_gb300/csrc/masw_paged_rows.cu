@@ -195,16 +195,22 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     }
     pdl_wait();
     pdl_trigger();
-    const int total = make_line<kThreads>(p, pre, s_kv, s_n, s_r0, blockIdx.x == 0);
+    const Line line = make_line<kThreads>(p, pre, s_kv, s_n, s_r0, blockIdx.x == 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
     Walk walk;
-    walk.t = first_tile(blockIdx.x, total, gridDim.x);
-    walk.t1 = first_tile(blockIdx.x + 1, total, gridDim.x);
-    {   // the sequence of the first tile
-        int lo = 0, hi = B;
+    if (const int per_pair = pair_ctas(B * Hkv, line.longest, line.total, gridDim.x)) {
+        const int pair = blockIdx.x / per_pair, part = blockIdx.x - pair * per_pair, h = pair % Hkv;
+        walk.b = imin(pair / Hkv, B - 1);
+        const int nt = pair < B * Hkv ? (pre[walk.b + 1] - pre[walk.b]) / Hkv : 0;
+        walk.t = pre[walk.b] + h * nt + part_first(part, nt, per_pair);
+        walk.t1 = pre[walk.b] + h * nt + part_first(part + 1, nt, per_pair);
+    } else {
+        walk.t = first_tile(blockIdx.x, line.total, gridDim.x);
+        walk.t1 = first_tile(blockIdx.x + 1, line.total, gridDim.x);
+        int lo = 0, hi = B;   // the sequence of the first tile
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (pre[mid] <= walk.t) lo = mid;
@@ -810,54 +816,67 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     }
 }
 
-// Joins the pieces of the pairs that were cut.  CTA (pair, row); thread d owns
-// output element d.
+// Joins the pieces of the pairs that were cut.  CTA (pair, rows): D / 4 threads own
+// a row, four output elements each.
+constexpr int kMergeThreads = 256, kAtOnce = 8;
 template <int D>
-__global__ void __launch_bounds__(128) rows_merge_kernel(const __grid_constant__ PagedAttnParams p, int n_cta) {
+__global__ void __launch_bounds__(kMergeThreads) rows_merge_kernel(const __grid_constant__ PagedAttnParams p, int n_cta) {
     __shared__ int pre[MASW_MAX_BATCH + 1], s_kv[MASW_MAX_BATCH], s_n[MASW_MAX_BATCH], s_r0[MASW_MAX_BATCH];
-    const int tid = threadIdx.x, b = blockIdx.x / p.c.Hkv, h = blockIdx.x % p.c.Hkv, G = p.G;
-    const int total = make_line<128>(p, pre, s_kv, s_n, s_r0, false);
-    const int per = (pre[b + 1] - pre[b]) / p.c.Hkv, T0 = pre[b] + h * per, T1 = T0 + per, nq = s_n[b] * G;
+    const int pair = blockIdx.x, b = pair / p.c.Hkv, h = pair % p.c.Hkv, G = p.G;
+    const int r = blockIdx.y * (kMergeThreads * 4 / D) + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    const Line line = make_line<kMergeThreads>(p, pre, s_kv, s_n, s_r0, false);
+    const int nt = (pre[b + 1] - pre[b]) / p.c.Hkv, T0 = pre[b] + h * nt, nq = s_n[b] * G;
+    const int per_pair = pair_ctas(p.c.B * p.c.Hkv, line.longest, line.total, n_cta);
+    int c0 = 0, c1 = 0;
+    if (nt > 0) {
+        c0 = per_pair ? pair * per_pair : tile_owner(T0, line.total, n_cta);
+        c1 = per_pair ? c0 + imin(nt, per_pair) - 1 : tile_owner(T0 + nt - 1, line.total, n_cta);
+    }
     pdl_wait();
     pdl_trigger();
-    if (per == 0) return;
-    const int c0 = tile_owner(T0, total, n_cta), c1 = tile_owner(T1 - 1, total, n_cta);
-    if (c0 == c1) return;
-    const int r = blockIdx.y;
-    if (r >= nq) return;
-    float M = -INFINITY, l = 0.f, o = 0.f;
-    for (int c8 = c0; c8 <= c1; c8 += 10) {
-        float pm[10], pl[10], po[10];
+    if (c0 == c1 || r >= nq) return;
+    float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c8 = c0; c8 <= c1; c8 += kAtOnce) {
+        float pm[kAtOnce], pl[kAtOnce];
+        float4 po[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < 10; ++k) {
-            const int c = c8 + k;
+        for (int k = 0; k < kAtOnce; ++k) {
             pm[k] = -INFINITY;
-            pl[k] = po[k] = 0.f;
-            if (c <= c1) {
-                const float* part = p.part + ((size_t)c * 2 + (T0 <= first_tile(c, total, n_cta) ? 0 : 1)) * kRowsMax * (D + 2);
+            pl[k] = 0.f;
+            po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c8 + k <= c1) {
+                const int c = c8 + k;
+                const int slot = per_pair || T0 <= first_tile(c, line.total, n_cta) ? 0 : 1;
+                const float* part = p.part + ((size_t)c * 2 + slot) * kRowsMax * (D + 2);
                 pm[k] = __ldcg(part + kRowsMax * D + r);
                 pl[k] = __ldcg(part + kRowsMax * (D + 1) + r);
-                po[k] = __ldcg(part + r * D + tid % D);
+                po[k] = __ldcg(reinterpret_cast<const float4*>(part + r * D + d));
             }
         }
-        float m8 = M;
+        float top = M;
 #pragma unroll
-        for (int k = 0; k < 10; ++k) m8 = fmaxf(m8, pm[k]);
-        if (m8 == -INFINITY) continue;
-        const float w = exp2f(M - m8);
+        for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, pm[k]);
+        if (top == -INFINITY) continue;
+        const float w = exp2f(M - top);
         l *= w;
-        o *= w;
-        M = m8;
 #pragma unroll
-        for (int k = 0; k < 10; ++k) {
+        for (int e = 0; e < 4; ++e) o[e] *= w;
+        M = top;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
             const float wk = exp2f(pm[k] - M);
             l = fmaf(pl[k], wk, l);
-            o = pm[k] == -INFINITY ? o : fmaf(po[k], wk, o);
+            if (pm[k] == -INFINITY) continue;
+            o[0] = fmaf(po[k].x, wk, o[0]);
+            o[1] = fmaf(po[k].y, wk, o[1]);
+            o[2] = fmaf(po[k].z, wk, o[2]);
+            o[3] = fmaf(po[k].w, wk, o[3]);
         }
     }
     const size_t row = (size_t)(s_r0[b] + r / G) * p.Hq + h * G + r % G;
-    if (tid < D) store_out(p, row * D + tid, l == 0.f ? 0.f : o / l);
-    if (tid == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) store_out(p, row * D + d + e, l == 0.f ? 0.f : o[e] / l);
+    if (d == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
 }
 
 template <bool E4, int D, int NP>
@@ -874,8 +893,9 @@ cudaError_t launch(const PagedAttnParams& p, int n_cta, cudaStream_t st) {
     }
     e = masw_launch(rows_kernel<E4, D, NP>, dim3(n_cta), dim3(kThreads), C::kSmem, st, 1, p);
     if (e != cudaSuccess) return e;
-    const int nq = p.max_rows * p.G;
-    return masw_launch(rows_merge_kernel<D>, dim3(p.c.B * p.c.Hkv, nq), dim3(128), 0, st, 1, p, n_cta);
+    constexpr int kRows = kMergeThreads * 4 / D;
+    return masw_launch(rows_merge_kernel<D>, dim3(p.c.B * p.c.Hkv, (p.max_rows * p.G + kRows - 1) / kRows), dim3(kMergeThreads), 0,
+                       st, 1, p, n_cta);
 }
 
 }  // namespace rows

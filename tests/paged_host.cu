@@ -64,6 +64,25 @@ int main() {
         while (e < 119 && (double)a > 448.0 * std::ldexp(1.0, e)) ++e;
         wrong += pow2_scale_exp(bits) != e;
     }
+    // shares of tiles: every tile once, its owner found again
+    long torn = 0;
+    for (int i = 0; i < 3000; ++i) {
+        const int C = 1 + upto(200), total = upto(i % 2 ? 300 : 200000), nt = 1 + upto(i % 2 ? 20 : 5000), s = 1 + upto(160);
+        torn += first_tile(0, total, C) != 0 || first_tile(C, total, C) != total;
+        for (int c = 0; c < C; ++c) {
+            const int a = first_tile(c, total, C), b = first_tile(c + 1, total, C);
+            torn += b < a || b - a > total / C + 1;
+            if (b > a) torn += tile_owner(a, total, C) != c || tile_owner(b - 1, total, C) != c;
+        }
+        torn += part_first(0, nt, s) != 0 || part_first(s, nt, s) != nt;
+        for (int k = 0; k < s; ++k) {
+            const int n = part_first(k + 1, nt, s) - part_first(k, nt, s);
+            torn += n < 0 || n > (nt + s - 1) / s || (n > 0) != (k < nt);
+        }
+        const int pairs = 1 + upto(300), own = pair_ctas(pairs, nt, total, C);
+        torn += own < 0 || own * pairs > C || (own && (nt + own - 1) / own > total / C + kUneven);
+    }
+    std::printf("torn_shares %ld\n", torn);
     std::printf("scales %ld\nwrong_scales %ld\nzero_scale %d\n", scales, wrong, pow2_scale_exp(0));
     return 0;
 }
