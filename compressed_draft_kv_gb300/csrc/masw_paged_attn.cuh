@@ -166,10 +166,10 @@ __device__ Line make_line(const PagedAttnParams& p, int* pre, int* s_kv, int* s_
 }
 
 // How the many-rows kernel cuts its work: `items` of 256 rows a (sequence, kv head)
-// pair; of all pairs' items, the first `whole` take a CTA each and the last `cut`
-// are cut along the keys into n_split CTAs.
+// pair, in the order of unit_of; the first `whole` units take a CTA each and the last
+// `cut` n_split CTAs, along the keys if they have at least min_tiles tiles of them.
 struct TilePlan {
-    int items, whole, cut, n_split;
+    int items, group, whole, cut, n_split, min_tiles;
 };
 // The many-rows kernel and its merge (masw_paged_tile.cu).
 cudaError_t launch_paged_tiles(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st);
