@@ -299,6 +299,17 @@ def test_long_blocks_ragged(d, dtype, hkv, g, page):
 
 
 @pytest.mark.parametrize("d,dtype", KINDS)
+@pytest.mark.parametrize("n,kv,g,page,window,o_dtype", [
+    ([9, 16, 17], [9, 200, 385], 4, 64, 0, torch.bfloat16), ([33, 20, 1], [2001, 129, 1], 2, 16, 0, torch.float32),
+    ([32, 31, 9], [1500, 31, 256], 4, 32, 100, torch.bfloat16), ([16, 1, 12], [4000, 128, 700], 8, 128, 300, torch.float32),
+    ([90, 64, 50], [640, 64, 300], 1, 64, 0, torch.bfloat16)])
+def test_blocks_of_one_tile_of_rows(d, dtype, n, kv, g, page, window, o_dtype):
+    """More rows than the few-rows kernel takes and at most 128: one tile, or two where a sequence has more."""
+    c = Cache(kv, 2, d, page, dtype, seed=62)
+    run_attention(c, kv, n, 2 * g, seed=63, window=window, o_dtype=o_dtype, pad=2)
+
+
+@pytest.mark.parametrize("d,dtype", KINDS)
 @pytest.mark.parametrize("n,window", [([1, 1, 1], 1), ([1, 1, 1], 100), ([3, 2, 8], 128), ([3, 2, 8], 5), ([150, 40, 1], 64),
                                       ([150, 40, 1], 129), ([150, 40, 1], 100000)])
 def test_sliding_window(d, dtype, n, window):
