@@ -302,6 +302,8 @@ def masw_paged_cache(k, v, page_table, k_scale=None, v_scale=None) -> masw_paged
     for x in (k, v):
         if tuple(x.stride()[1:]) != (p * d, d, 1):
             raise ValueError("a page must be dense")
+        if n > 1 and x.stride(0) < h * p * d:
+            raise ValueError("pages must not overlap")
     if e4:
         for x in (k_scale, v_scale):
             if x is None or x.dtype != torch.float32 or tuple(x.shape) != (n, h) or not x.is_contiguous():
@@ -332,7 +334,7 @@ def masw_rope(cos_sin, interleaved=False) -> masw_rope_t:
         raise ValueError("cos_sin must be contiguous fp32 [n_pos, rot_dim]")
     r = masw_rope_t(_ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved))
     r.tensors = [cos_sin]
-    r.address = ctypes.addressof(r)
+    r.address, r.device = ctypes.addressof(r), cos_sin.device
     return r
 
 
@@ -343,7 +345,11 @@ def _token_rows(name, x, heads, dim, cache):
         raise ValueError(f"{name} must be bfloat16 [rows, {heads}, {dim}] on the cache's device")
     if st[2] != 1 or (st[1] != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return st[0] if shape[0] > 1 else 0
+    if shape[0] < 2:
+        return 0
+    if st[0] < heads * dim:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return st[0]
 
 
 def _ints(name, x, n, cache):
@@ -376,11 +382,13 @@ def masw_paged_append(cache, kv_len, k, v, rope=None, pos=None, q=None, q_out=No
     if q is not None:
         hq = q.shape[1]
         qs = _token_rows("q", q, hq, D, cache)
-        if q_out is None or q_out.dtype is not cache.bf16 or q_out.shape != q.shape or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous bfloat16 of q's shape")
+        if q_out is None or q_out.dtype is not cache.bf16 or q_out.shape != q.shape or not q_out.is_contiguous() or q_out.device != cache.device:
+            raise ValueError("q_out must be contiguous bfloat16 of q's shape on the cache's device")
         q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
     if v.shape[0] != rows or (q is not None and q.shape[0] != rows):
         raise ValueError("k, v and q differ in rows")
+    if rope is not None and rope.device != cache.device:
+        raise ValueError("the rotary table lies on another device than the cache")
     _check(load().masw_paged_append(cache.address, _ints("kv_len", kv_len, B, cache), _ints("row_start", row_start, B + 1, cache),
                                     rows, k.data_ptr(), v.data_ptr(), ks, vs, None if rope is None else rope.address,
                                     _ints("pos", pos, rows, cache), q_ptr, q_out_ptr, hq, qs,
@@ -402,7 +410,7 @@ def masw_paged_attn(cache, kv_len, q, o, lse=None, row_start=None, max_rows=None
     B = cache.batch
     qs = _token_rows("q", q, hq, cache.head_dim, cache)
     if o.shape != q.shape or not o.is_contiguous() or o.device != cache.device or (o.dtype is not cache.bf16 and o.dtype is not cache.f32):
-        raise ValueError("o must be contiguous bfloat16 or float32 of q's shape")
+        raise ValueError("o must be contiguous bfloat16 or float32 of q's shape on the cache's device")
     lse_ptr = None
     if lse is not None:
         if lse.shape != (rows, hq) or lse.dtype is not cache.f32 or not lse.is_contiguous() or lse.device != cache.device:
@@ -412,6 +420,8 @@ def masw_paged_attn(cache, kv_len, q, o, lse=None, row_start=None, max_rows=None
     if workspace is None:
         import torch
         workspace = torch.empty(masw_paged_workspace_bytes(cache, rows, mr, hq), dtype=torch.uint8, device=cache.device)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
     _check(load().masw_paged_attn(cache.address, _ints("kv_len", kv_len, B, cache), _ints("row_start", row_start, B + 1, cache),
                                   rows, mr, q.data_ptr(), hq, qs, window, scale, o.data_ptr(),
                                   MASW_BF16 if o.dtype is cache.bf16 else MASW_F32, lse_ptr,

@@ -103,6 +103,27 @@ def test_binding_refusals():
             capi.masw_paged_attn(ok, stream=0, workspace=torch.zeros(16, dtype=torch.uint8), **a)
 
 
+def test_binding_refuses_what_would_be_read_out_of_range():
+    """Broadcast rows and pages, whose stride of 0 would read as dense, and tensors on another device."""
+    k, table = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32)
+    one = k[:1].expand(4, 2, 16, 64)
+    with pytest.raises(ValueError):
+        capi.masw_paged_cache(one, one, table)
+    c = capi.masw_paged_cache(k, k, table)
+    x, n = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    row, there = x[:1].expand(4, 2, 64), dict(dtype=torch.bfloat16, device="meta")
+    away = capi.masw_rope(torch.zeros(4, 64))
+    away.device = torch.device("meta")
+    for kw in (dict(k=row), dict(v=row), dict(q=row, q_out=x), dict(q=x, q_out=torch.zeros(4, 2, 64, **there)), dict(rope=away),
+               dict(k=torch.zeros(4, 2, 64, **there)), dict(kv_len=n.to("meta"))):
+        with pytest.raises(ValueError):
+            capi.masw_paged_append(c, stream=0, **(dict(kv_len=n, k=x, v=x) | kw))
+    ws = torch.zeros(64, dtype=torch.uint8)
+    for kw in (dict(q=row), dict(workspace=ws.to("meta")), dict(workspace=ws[::2]), dict(o=x.to("meta"))):
+        with pytest.raises(ValueError):
+            capi.masw_paged_attn(c, stream=0, **(dict(kv_len=n, q=x, o=torch.zeros_like(x), workspace=ws) | kw))
+
+
 def test_unit_map_scales_and_chunks(tmp_path):
     """The append's grid covers every touched page once, the scale exponents match a search, and the lanes of a head
     cover its elements once with paired chunks."""
