@@ -419,6 +419,8 @@ def masw_paged_attn(cache, kv_len, q, o, lse=None, row_start=None, max_rows=None
     mr = rows // B if row_start is None else (rows if max_rows is None else max_rows)
     if workspace is None:
         import torch
+        if stream is not None and cache.cuda_index is not None and stream != torch._C._cuda_getCurrentRawStream(cache.cuda_index):
+            raise ValueError("on a stream other than the current one the call needs a workspace")   # it would be reused too early
         workspace = torch.empty(masw_paged_workspace_bytes(cache, rows, mr, hq), dtype=torch.uint8, device=cache.device)
     elif workspace.device != cache.device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")

@@ -25,6 +25,12 @@
 // Rows behind the end of a sequence never count: their scores are masked, and
 // their V rows are zeroed in shared memory (0 x NaN is NaN in a matrix product).
 //
+// Measured: decode of 8 sequences at 32K, 24 query and 8 kv heads of 128, e4m3: 87 us
+// (6.2 TB/s); 32 sequences of 4K to 16K, 32 query heads, bf16: 211 us (6.7 TB/s, the rate
+// of a copy); verify, 6 rows of 4 sequences at 32K, e4m3: 62 us (4.3 TB/s: the softmax
+// of 24 rows, not the stream).  The smallest calls (one sequence at 4K: 11 us) are a chain
+// of latencies: launch, lengths, page ids, scales, pages, scores, merge.
+//
 // Warps 0-3 and 4-7: two softmax groups that take the tiles in turn, each with its
 // own S, P, O, sums and reference (a tile's chain of barriers, votes and TMEM
 // loads is ~1000 cycles long whatever the work in it; one group alone left half of
@@ -224,285 +230,285 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 
     // one register change for each whole group of four warps
     if (warp >= 8) {
-    give_registers<NP>();
-    if (warp == 8) {
-        // ---------------- S^T = K Q^T ----------------
-        int i = 0, piece = 0;
-        while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
-            const int qb = piece % C::kQBufs;
-            ok = all(wait(C::kQFull + qb, piece / C::kQBufs));
-            const uint64_t bq = smem_desc(sb + C::kOffQ + qb * C::kQBuf, 128, (C::kRB / 16) * 128, 0);
-            for (int j = 0; ok && j < walk.nt; ++j, ++i) {
-                const int st = i % C::kKS, sbuf = i & 1;
-                ok = all(wait(C::kKFull + st, i / C::kKS)) && (i < 2 || all(wait(C::kSFree + sbuf, i / 2 - 1)));
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t ak = smem_desc(sb + C::kOffK + st * C::kTileB, 16, C::kAtom, C::kSwz);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < C::kRB / 32; ++kk) {
-                        const uint64_t a = ak + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
-                        const uint64_t b = bq + (uint64_t)((kk * 256) >> 4);
-                        if (E4) umma_f8(tmem + sbuf * C::kSN, a, b, C::kIdescS, kk > 0);
-                        else umma_bf16(tmem + sbuf * C::kSN, a, b, C::kIdescS, kk > 0);
-                    }
-                    umma_commit(bar_at(C::kSFull + sbuf));
-                    umma_commit(bar_at(C::kKFree + st));
-                    if (j + 1 == walk.nt) umma_commit(bar_at(C::kQFree + qb));
-                }
-                __syncwarp();
-            }
-            ++piece;
-        }
-        // nothing may arrive on a barrier after the CTA ended
-        if (ok && i > 0)
-            ok = all(wait(C::kKFree + (i - 1) % C::kKS, (i - 1) / C::kKS)) &&
-                 all(wait(C::kQFree + (piece - 1) % C::kQBufs, (piece - 1) / C::kQBufs));
-        if (!ok) {   // let the matrix products in flight end before the CTA does
-            st_shared_u32(abort_flag, 1u);
-            if (elect_one()) umma_commit(bar_at(C::kDone));
-            __syncwarp();
-            mbar_wait(bars + C::kDone, 0, nullptr);
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        // ---------------- O^T += V^T P^T, and Q of the next piece ----------------
-        // Q in 16-byte chunks: a row is kLanes of them, a pass kPer rows; every lane
-        // splits the chunks that it copied itself.  Loops stay rolled, here and wherever
-        // code runs once a piece: fetching instructions for the first time costs more
-        // than running them.  The copies of the next piece's
-        // rows are issued at a piece's start and finished after its second tile.
-        constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPass = NP / kPer;
-        const int e0 = (lane % kLanes) * 8, rl = lane / kLanes;
-        const uint32_t raw = sb + C::kOffQRaw + (uint32_t)lane * 16u;   // pass s: 512 bytes further
-        Walk wq = walk;
-        int q_piece = 0;
-        // K-major core matrices of 8 rows x 16 bytes, consecutive along the row
-        auto at = [&](int row, int byte) {
-            return sb + C::kOffQ + (q_piece % C::kQBufs) * C::kQBuf +
-                   (uint32_t)((row >> 3) * (C::kRB / 16) * 128 + (byte >> 4) * 128 + (row & 7) * 16 + (byte & 15));
-        };
-        auto q_free = [&]() {
-            return q_piece < C::kQBufs || all(wait(C::kQFree + q_piece % C::kQBufs, q_piece / C::kQBufs - 1));
-        };
-        auto q_issue = [&]() {
-            if (!next_piece(wq, pre, B, Hkv, s_kv, s_n, p.window)) return false;
-            // bf16: straight into the operand, once the matrix products that read it are
-            // done; with one buffer that is at the end of the piece
-            if (!E4 && C::kQBufs > 1) ok = q_free();
-            const int nq = s_n[wq.b] * G, r0 = s_r0[wq.b];
-            int tok = rl / G, g = rl - tok * G;
-#pragma unroll 1
-            for (int s = 0; s < kPass; ++s) {
-                const int r = s * kPer + rl;
-                const bool in = r < nq;
-                const __nv_bfloat16* src = p.q + (size_t)(r0 + (in ? tok : 0)) * p.q_stride + (size_t)(wq.h * G + (in ? g : 0)) * D + e0;
-                if (E4 || C::kQBufs == 1) {
-                    cp_async16(raw + s * 512, src, in ? 16 : 0);
-                } else {
-                    cp_async16(at(r, e0 * 2), src, in ? 16 : 0);
-                    if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
-                }
-                g += kPer;
-                while (g >= G) {
-                    g -= G;
-                    ++tok;
-                }
-            }
-            cp_async_commit();
-            return true;
-        };
-        auto q_finish = [&]() {
-            cp_async_wait<0>();
-            float inv = 1.f;
-            if constexpr (E4) {
-                float amax = 0.f;
-#pragma unroll 1
-                for (int s = 0; s < kPass; ++s) {
-                    const float4 v = ld_shared_v4f(raw + s * 512);
-                    float f[8];
-                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
-                }
-#pragma unroll
-                for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                inv = 1.f / pow2_scale(amax);
-                ok = ok && q_free();
-#pragma unroll 1
-                for (int s = 0; s < kPass; ++s) {
-                    const int r = s * kPer + rl;
-                    const float4 v = ld_shared_v4f(raw + s * 512);
-                    float f[8];
-                    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
-                    uint32_t w1[4], w2[4];
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float a = f[e] * inv, b = f[e + 1] * inv;
-                        const uint32_t q1 = e4m3x2(a, b);
-                        float a1, b1;
-                        f16x2_to_f32(e4m3x2_to_f16x2(q1), a1, b1);
-                        w1[e / 2] = q1;
-                        w2[e / 2] = e4m3x2((a - a1) * 16.f, (b - b1) * 16.f);
-                    }
-                    st_shared_v2(at(r, e0), w1[0] | (w1[1] << 16), w1[2] | (w1[3] << 16));
-                    st_shared_v2(at(NP + r, e0), w2[0] | (w2[1] << 16), w2[2] | (w2[3] << 16));
-                }
-            } else if constexpr (C::kQBufs == 1) {
-                ok = ok && q_free();
-#pragma unroll 1
-                for (int s = 0; s < kPass; ++s) {
-                    const int r = s * kPer + rl;
-                    const float4 v = ld_shared_v4f(raw + s * 512);
-                    const uint4 x = *reinterpret_cast<const uint4*>(&v);
-                    st_shared_v4(at(r, e0 * 2), x.x, x.y, x.z, x.w);
-                    if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
-                }
-            }
-            if (!ok) return;
-            const int qb = q_piece % C::kQBufs;
-            if (lane == 0) qscale[qb] = p.scale_log2 / inv;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_at(C::kQFull + qb));
-            ++q_piece;
-        };
-        // one operand buffer: it is free only when the piece's own products are done
-        constexpr bool kLate = C::kQBufs == 1;
-        if (q_issue()) q_finish();
-        int i = 0;
-        while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
-            bool pending = q_issue();
-            for (int j = 0; ok && j < walk.nt; ++j, ++i) {
-                const int st = i % C::kVS, pb = i & 1;
-                ok = all(wait(C::kPFull + pb, i / 2)) && all(wait(C::kVFull + st, i / C::kVS));
-                if (!ok) break;
-                tc_fence_after();
-                // head_dim 64: the second half of the 128 M rows repeats the first
-                // (a leading offset of 0); head_dim 128 in bf16: the second panel
-                const uint64_t av = smem_desc(sb + C::kOffV + st * C::kTileB, C::kPanels == 2 ? C::kPanel : 0, C::kAtom, C::kSwz);
-                const uint64_t bp = smem_desc(sb + C::kOffP + pb * C::kPBuf, 128, 2048, 0);
-                constexpr int kKeys = 32 / C::kES;   // keys of one matrix instruction
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < kTile / kKeys; ++kk) {
-                        const uint64_t a = av + (uint64_t)((kk * kKeys * C::kPB) >> 4);
-                        const uint64_t b = bp + (uint64_t)((kk * kKeys * 16) >> 4);
-                        if (E4) umma_f8(tmem + C::kColO + pb * C::kPN, a, b, C::kIdescO, j > 1 || kk > 0);
-                        else umma_bf16(tmem + C::kColO + pb * C::kPN, a, b, C::kIdescO, j > 1 || kk > 0);
-                    }
-                    umma_commit(bar_at(C::kPFree + pb));
-                    umma_commit(bar_at(C::kVFree + st));
-                }
-                __syncwarp();
-                if (pending && j + 1 == (kLate ? walk.nt : imin(2, walk.nt))) {
-                    q_finish();
-                    pending = false;
-                }
-            }
-        }
-        // nothing may arrive on a barrier after the CTA ended
-        if (ok && i > 0) ok = all(wait(C::kVFree + (i - 1) % C::kVS, (i - 1) / C::kVS));
-        if (!ok) {
-            st_shared_u32(abort_flag, 1u);
-            cp_async_wait<0>();
-            if (elect_one()) umma_commit(bar_at(C::kDone + 1));
-            __syncwarp();
-            mbar_wait(bars + C::kDone + 1, 0, nullptr);
-        }
-        __syncwarp();
-    } else {
-        // ---------------- page ids and TMA: warp 10 K and the scales, warp 11 V ----------------
-        // A lane holds the page of one box (at most 128 rows of a page); a batch
-        // is up to 32 boxes of a piece.  Page ids are loaded two batches ahead, scales
-        // one.
-        const bool is_v = warp == 11;
-        const int stages = is_v ? C::kVS : C::kKS, full = is_v ? C::kVFull : C::kKFull, freed = is_v ? C::kVFree : C::kKFree;
-        const uint32_t ring = sb + (is_v ? C::kOffV : C::kOffK);
-        const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
-        const bool scales = E4 && !is_v;
-        const int box = imin(c.P, kTile), bpt = kTile / box, bt = 32 / bpt;   // boxes a tile, tiles a batch
-        int left = 0, at = 0;            // tiles of the piece not yet in a batch, and the first of them
-        struct Batch { int h, tile, nt, pid, lo, hi; bool in; float ks, vs; };   // boxes [lo, hi) hold visible keys
-        auto next_batch = [&](Batch& x) {
-            x.nt = 0;
-            x.in = false;
-            if (left == 0) {
-                if (!next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) return;
-                left = walk.nt;
-                at = walk.tile;
-            }
-            x.h = walk.h;
-            x.tile = at;
-            x.nt = imin(left, bt);
-            at += x.nt;
-            left -= x.nt;
-            const TileRange r = tile_range(s_n[walk.b], s_kv[walk.b], p.window);
-            const int key0 = x.tile * kTile;
-            x.lo = imax(0, r.lo / c.P * c.P - key0) / box;   // pages wholly before the first visible key are left out
-            x.hi = imin(x.nt * bpt, (r.hi - key0 + box - 1) / box);
-            x.in = lane >= x.lo && lane < x.hi;
-            x.pid = x.in ? __ldg(c.table + (size_t)walk.b * c.table_stride + (key0 + lane * box) / c.P) : 0;
-        };
-        auto check_and_scale = [&](Batch& x) {
-            if (x.in && (x.pid < 0 || x.pid >= c.n_pages)) {
-                if (p.status) atomicExch(p.status, MASW_EINVAL);
-                x.pid = 0;
-            }
-            x.ks = x.vs = 1.f;
-            if (scales && x.in) {
-                x.ks = __ldg(c.k_scale + (size_t)x.pid * Hkv + x.h);
-                x.vs = __ldg(c.v_scale + (size_t)x.pid * Hkv + x.h);
-            }
-        };
-        Batch cur, nxt;
-        int i = 0, st = 0, turn = 0;     // tile, its stage, and how often the ring went round
-        next_batch(cur);
-        next_batch(nxt);
-        check_and_scale(cur);
-        while (ok && cur.nt > 0) {
-            check_and_scale(nxt);
-            Batch nn;
-            next_batch(nn);
-            for (int j = 0; j < cur.nt; ++j, ++i) {
-                const int b0 = imax(cur.lo, j * bpt), b1 = imin(cur.hi, (j + 1) * bpt);   // the tile's boxes
-                if (turn > 0) ok = all(wait(freed + st, turn - 1));
-                if (!ok) break;
-                if (elect_one()) mbar_expect_tx_at(bar_at(full + st), (uint32_t)(imax(0, b1 - b0) * box * C::kRB));
-                __syncwarp();
-                // the whole warp walks the boxes, one lane issues
-                for (int q = b0; q < b1; ++q) {
-                    const int pid = __shfl_sync(0xffffffffu, cur.pid, q);
-                    const int row = (cur.tile * kTile + q * box) & (c.P - 1);
-                    const uint32_t dst = ring + st * C::kTileB + (uint32_t)((q - j * bpt) * box * C::kPB);
+        give_registers<NP>();
+        if (warp == 8) {
+            // ---------------- S^T = K Q^T ----------------
+            int i = 0, piece = 0;
+            while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
+                const int qb = piece % C::kQBufs;
+                ok = all(wait(C::kQFull + qb, piece / C::kQBufs));
+                const uint64_t bq = smem_desc(sb + C::kOffQ + qb * C::kQBuf, 128, (C::kRB / 16) * 128, 0);
+                for (int j = 0; ok && j < walk.nt; ++j, ++i) {
+                    const int st = i % C::kKS, sbuf = i & 1;
+                    ok = all(wait(C::kKFull + st, i / C::kKS)) && (i < 2 || all(wait(C::kSFree + sbuf, i / 2 - 1)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ak = smem_desc(sb + C::kOffK + st * C::kTileB, 16, C::kAtom, C::kSwz);
                     if (elect_one()) {
 #pragma unroll
-                        for (int pn = 0; pn < C::kPanels; ++pn)
-                            tma_load_4d(dst + pn * C::kPanel, map, pn * C::kPB / C::kES, row, cur.h, pid, bar_at(full + st));
+                        for (int kk = 0; kk < C::kRB / 32; ++kk) {
+                            const uint64_t a = ak + (uint64_t)(((kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32) >> 4);
+                            const uint64_t b = bq + (uint64_t)((kk * 256) >> 4);
+                            if (E4) umma_f8(tmem + sbuf * C::kSN, a, b, C::kIdescS, kk > 0);
+                            else umma_bf16(tmem + sbuf * C::kSN, a, b, C::kIdescS, kk > 0);
+                        }
+                        umma_commit(bar_at(C::kSFull + sbuf));
+                        umma_commit(bar_at(C::kKFree + st));
+                        if (j + 1 == walk.nt) umma_commit(bar_at(C::kQFree + qb));
+                    }
+                    __syncwarp();
+                }
+                ++piece;
+            }
+            // nothing may arrive on a barrier after the CTA ended
+            if (ok && i > 0)
+                ok = all(wait(C::kKFree + (i - 1) % C::kKS, (i - 1) / C::kKS)) &&
+                     all(wait(C::kQFree + (piece - 1) % C::kQBufs, (piece - 1) / C::kQBufs));
+            if (!ok) {   // let the matrix products in flight end before the CTA does
+                st_shared_u32(abort_flag, 1u);
+                if (elect_one()) umma_commit(bar_at(C::kDone));
+                __syncwarp();
+                mbar_wait(bars + C::kDone, 0, nullptr);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ---------------- O^T += V^T P^T, and Q of the next piece ----------------
+            // Q in 16-byte chunks: a row is kLanes of them, a pass kPer rows; every lane
+            // splits the chunks that it copied itself.  Loops stay rolled, here and wherever
+            // code runs once a piece: fetching instructions for the first time costs more
+            // than running them.  The copies of the next piece's
+            // rows are issued at a piece's start and finished after its second tile.
+            constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPass = NP / kPer;
+            const int e0 = (lane % kLanes) * 8, rl = lane / kLanes;
+            const uint32_t raw = sb + C::kOffQRaw + (uint32_t)lane * 16u;   // pass s: 512 bytes further
+            Walk wq = walk;
+            int q_piece = 0;
+            // K-major core matrices of 8 rows x 16 bytes, consecutive along the row
+            auto at = [&](int row, int byte) {
+                return sb + C::kOffQ + (q_piece % C::kQBufs) * C::kQBuf +
+                       (uint32_t)((row >> 3) * (C::kRB / 16) * 128 + (byte >> 4) * 128 + (row & 7) * 16 + (byte & 15));
+            };
+            auto q_free = [&]() {
+                return q_piece < C::kQBufs || all(wait(C::kQFree + q_piece % C::kQBufs, q_piece / C::kQBufs - 1));
+            };
+            auto q_issue = [&]() {
+                if (!next_piece(wq, pre, B, Hkv, s_kv, s_n, p.window)) return false;
+                // bf16: straight into the operand, once the matrix products that read it are
+                // done; with one buffer that is at the end of the piece
+                if (!E4 && C::kQBufs > 1) ok = q_free();
+                const int nq = s_n[wq.b] * G, r0 = s_r0[wq.b];
+                int tok = rl / G, g = rl - tok * G;
+#pragma unroll 1
+                for (int s = 0; s < kPass; ++s) {
+                    const int r = s * kPer + rl;
+                    const bool in = r < nq;
+                    const __nv_bfloat16* src = p.q + (size_t)(r0 + (in ? tok : 0)) * p.q_stride + (size_t)(wq.h * G + (in ? g : 0)) * D + e0;
+                    if (E4 || C::kQBufs == 1) {
+                        cp_async16(raw + s * 512, src, in ? 16 : 0);
+                    } else {
+                        cp_async16(at(r, e0 * 2), src, in ? 16 : 0);
+                        if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
+                    }
+                    g += kPer;
+                    while (g >= G) {
+                        g -= G;
+                        ++tok;
                     }
                 }
-                __syncwarp();
-                if (scales) {   // behind the copies, which need not wait for them
-                    if (lane / bpt == j)
-                        st_shared_v4(sb + C::kOffMeta + (uint32_t)((i % kMeta) * 8 + lane % bpt) * 16u, __float_as_uint(cur.ks),
-                                     __float_as_uint(cur.vs == 1.f ? 0.f : __log2f(cur.vs)), __float_as_uint(__frcp_rn(cur.vs)), 0u);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
+                cp_async_commit();
+                return true;
+            };
+            auto q_finish = [&]() {
+                cp_async_wait<0>();
+                float inv = 1.f;
+                if constexpr (E4) {
+                    float amax = 0.f;
+#pragma unroll 1
+                    for (int s = 0; s < kPass; ++s) {
+                        const float4 v = ld_shared_v4f(raw + s * 512);
+                        float f[8];
+                        Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(f[e]));
+                    }
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    inv = 1.f / pow2_scale(amax);
+                    ok = ok && q_free();
+#pragma unroll 1
+                    for (int s = 0; s < kPass; ++s) {
+                        const int r = s * kPer + rl;
+                        const float4 v = ld_shared_v4f(raw + s * 512);
+                        float f[8];
+                        Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
+                        uint32_t w1[4], w2[4];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const float a = f[e] * inv, b = f[e + 1] * inv;
+                            const uint32_t q1 = e4m3x2(a, b);
+                            float a1, b1;
+                            f16x2_to_f32(e4m3x2_to_f16x2(q1), a1, b1);
+                            w1[e / 2] = q1;
+                            w2[e / 2] = e4m3x2((a - a1) * 16.f, (b - b1) * 16.f);
+                        }
+                        st_shared_v2(at(r, e0), w1[0] | (w1[1] << 16), w1[2] | (w1[3] << 16));
+                        st_shared_v2(at(NP + r, e0), w2[0] | (w2[1] << 16), w2[2] | (w2[3] << 16));
+                    }
+                } else if constexpr (C::kQBufs == 1) {
+                    ok = ok && q_free();
+#pragma unroll 1
+                    for (int s = 0; s < kPass; ++s) {
+                        const int r = s * kPer + rl;
+                        const float4 v = ld_shared_v4f(raw + s * 512);
+                        const uint4 x = *reinterpret_cast<const uint4*>(&v);
+                        st_shared_v4(at(r, e0 * 2), x.x, x.y, x.z, x.w);
+                        if (NP + r < C::kSN) st_shared_v4(at(NP + r, e0 * 2), 0u, 0u, 0u, 0u);
+                    }
                 }
-                if (++st == stages) {
-                    st = 0;
-                    ++turn;
+                if (!ok) return;
+                const int qb = q_piece % C::kQBufs;
+                if (lane == 0) qscale[qb] = p.scale_log2 / inv;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_at(C::kQFull + qb));
+                ++q_piece;
+            };
+            // one operand buffer: it is free only when the piece's own products are done
+            constexpr bool kLate = C::kQBufs == 1;
+            if (q_issue()) q_finish();
+            int i = 0;
+            while (ok && next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) {
+                bool pending = q_issue();
+                for (int j = 0; ok && j < walk.nt; ++j, ++i) {
+                    const int st = i % C::kVS, pb = i & 1;
+                    ok = all(wait(C::kPFull + pb, i / 2)) && all(wait(C::kVFull + st, i / C::kVS));
+                    if (!ok) break;
+                    tc_fence_after();
+                    // head_dim 64: the second half of the 128 M rows repeats the first
+                    // (a leading offset of 0); head_dim 128 in bf16: the second panel
+                    const uint64_t av = smem_desc(sb + C::kOffV + st * C::kTileB, C::kPanels == 2 ? C::kPanel : 0, C::kAtom, C::kSwz);
+                    const uint64_t bp = smem_desc(sb + C::kOffP + pb * C::kPBuf, 128, 2048, 0);
+                    constexpr int kKeys = 32 / C::kES;   // keys of one matrix instruction
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < kTile / kKeys; ++kk) {
+                            const uint64_t a = av + (uint64_t)((kk * kKeys * C::kPB) >> 4);
+                            const uint64_t b = bp + (uint64_t)((kk * kKeys * 16) >> 4);
+                            if (E4) umma_f8(tmem + C::kColO + pb * C::kPN, a, b, C::kIdescO, j > 1 || kk > 0);
+                            else umma_bf16(tmem + C::kColO + pb * C::kPN, a, b, C::kIdescO, j > 1 || kk > 0);
+                        }
+                        umma_commit(bar_at(C::kPFree + pb));
+                        umma_commit(bar_at(C::kVFree + st));
+                    }
+                    __syncwarp();
+                    if (pending && j + 1 == (kLate ? walk.nt : imin(2, walk.nt))) {
+                        q_finish();
+                        pending = false;
+                    }
                 }
             }
-            cur = nxt;
-            nxt = nn;
+            // nothing may arrive on a barrier after the CTA ended
+            if (ok && i > 0) ok = all(wait(C::kVFree + (i - 1) % C::kVS, (i - 1) / C::kVS));
+            if (!ok) {
+                st_shared_u32(abort_flag, 1u);
+                cp_async_wait<0>();
+                if (elect_one()) umma_commit(bar_at(C::kDone + 1));
+                __syncwarp();
+                mbar_wait(bars + C::kDone + 1, 0, nullptr);
+            }
+            __syncwarp();
+        } else {
+            // ---------------- page ids and TMA: warp 10 K and the scales, warp 11 V ----------------
+            // A lane holds the page of one box (at most 128 rows of a page); a batch
+            // is up to 32 boxes of a piece.  Page ids are loaded two batches ahead, scales
+            // one.
+            const bool is_v = warp == 11;
+            const int stages = is_v ? C::kVS : C::kKS, full = is_v ? C::kVFull : C::kKFull, freed = is_v ? C::kVFree : C::kKFree;
+            const uint32_t ring = sb + (is_v ? C::kOffV : C::kOffK);
+            const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
+            const bool scales = E4 && !is_v;
+            const int box = imin(c.P, kTile), bpt = kTile / box, bt = 32 / bpt;   // boxes a tile, tiles a batch
+            int left = 0, at = 0;            // tiles of the piece not yet in a batch, and the first of them
+            struct Batch { int h, tile, nt, pid, lo, hi; bool in; float ks, vs; };   // boxes [lo, hi) hold visible keys
+            auto next_batch = [&](Batch& x) {
+                x.nt = 0;
+                x.in = false;
+                if (left == 0) {
+                    if (!next_piece(walk, pre, B, Hkv, s_kv, s_n, p.window)) return;
+                    left = walk.nt;
+                    at = walk.tile;
+                }
+                x.h = walk.h;
+                x.tile = at;
+                x.nt = imin(left, bt);
+                at += x.nt;
+                left -= x.nt;
+                const TileRange r = tile_range(s_n[walk.b], s_kv[walk.b], p.window);
+                const int key0 = x.tile * kTile;
+                x.lo = imax(0, r.lo / c.P * c.P - key0) / box;   // pages wholly before the first visible key are left out
+                x.hi = imin(x.nt * bpt, (r.hi - key0 + box - 1) / box);
+                x.in = lane >= x.lo && lane < x.hi;
+                x.pid = x.in ? __ldg(c.table + (size_t)walk.b * c.table_stride + (key0 + lane * box) / c.P) : 0;
+            };
+            auto check_and_scale = [&](Batch& x) {
+                if (x.in && (x.pid < 0 || x.pid >= c.n_pages)) {
+                    if (p.status) atomicExch(p.status, MASW_EINVAL);
+                    x.pid = 0;
+                }
+                x.ks = x.vs = 1.f;
+                if (scales && x.in) {
+                    x.ks = __ldg(c.k_scale + (size_t)x.pid * Hkv + x.h);
+                    x.vs = __ldg(c.v_scale + (size_t)x.pid * Hkv + x.h);
+                }
+            };
+            Batch cur, nxt;
+            int i = 0, st = 0, turn = 0;     // tile, its stage, and how often the ring went round
+            next_batch(cur);
+            next_batch(nxt);
+            check_and_scale(cur);
+            while (ok && cur.nt > 0) {
+                check_and_scale(nxt);
+                Batch nn;
+                next_batch(nn);
+                for (int j = 0; j < cur.nt; ++j, ++i) {
+                    const int b0 = imax(cur.lo, j * bpt), b1 = imin(cur.hi, (j + 1) * bpt);   // the tile's boxes
+                    if (turn > 0) ok = all(wait(freed + st, turn - 1));
+                    if (!ok) break;
+                    if (elect_one()) mbar_expect_tx_at(bar_at(full + st), (uint32_t)(imax(0, b1 - b0) * box * C::kRB));
+                    __syncwarp();
+                    // the whole warp walks the boxes, one lane issues
+                    for (int q = b0; q < b1; ++q) {
+                        const int pid = __shfl_sync(0xffffffffu, cur.pid, q);
+                        const int row = (cur.tile * kTile + q * box) & (c.P - 1);
+                        const uint32_t dst = ring + st * C::kTileB + (uint32_t)((q - j * bpt) * box * C::kPB);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int pn = 0; pn < C::kPanels; ++pn)
+                                tma_load_4d(dst + pn * C::kPanel, map, pn * C::kPB / C::kES, row, cur.h, pid, bar_at(full + st));
+                        }
+                    }
+                    __syncwarp();
+                    if (scales) {   // behind the copies, which need not wait for them
+                        if (lane / bpt == j)
+                            st_shared_v4(sb + C::kOffMeta + (uint32_t)((i % kMeta) * 8 + lane % bpt) * 16u, __float_as_uint(cur.ks),
+                                         __float_as_uint(cur.vs == 1.f ? 0.f : __log2f(cur.vs)), __float_as_uint(__frcp_rn(cur.vs)), 0u);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_at(C::kMetaBar + i % kMeta));
+                    }
+                    if (++st == stages) {
+                        st = 0;
+                        ++turn;
+                    }
+                }
+                cur = nxt;
+                nxt = nn;
+            }
+            // after a wait gave up, and at the end: no copy may be in flight when the CTA ends
+            if (!ok) st_shared_u32(abort_flag, 1u);
+            for (int k = imax(0, i - stages); k < i; ++k)
+                mbar_wait(bars + full + k % stages, (uint32_t)(k / stages) & 1u, nullptr);
+            __syncwarp();
         }
-        // after a wait gave up, and at the end: no copy may be in flight when the CTA ends
-        if (!ok) st_shared_u32(abort_flag, 1u);
-        for (int k = imax(0, i - stages); k < i; ++k)
-            mbar_wait(bars + full + k % stages, (uint32_t)(k / stages) & 1u, nullptr);
-        __syncwarp();
-    }
     } else {
         take_registers<NP>();
         // ---------------- softmax: thread wt of a group owns key wt of the group's tiles ----------------

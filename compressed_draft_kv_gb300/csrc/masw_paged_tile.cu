@@ -25,8 +25,13 @@
 // both interleaved, ended together, and left the tensor cores idle during both
 // softmaxes); 17 watches K and V for it, so that one barrier stands before a step.  18: page ids,
 // scales and K; 19: page ids and V; 20-23 widen V and clear the rows that no query
-// sees.  A long cache under few
-// rows is cut into splits, whose partial results a second kernel joins.
+// sees.  A long cache under few rows is cut into splits, whose partial results a second
+// kernel joins.
+//
+// Measured: a 2K chunk at 32K, 32 query and 8 kv heads of 128, e4m3: 774 us (1376
+// TFLOP/s); prompts of up to 4K, 24 query heads, bf16: 235 us (870 TFLOP/s: a CTA's start
+// and end, ~9 us, against a mean of 8 tiles of keys).  A tile of keys for both tiles
+// of rows takes ~2.9K cycles, of which the matrix products are ~2.1K.
 #include "masw_paged_attn.cuh"
 
 namespace masw {

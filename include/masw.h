@@ -323,8 +323,9 @@ int masw_verify_attn_noalloc(const void* q, const void* k_cache, const void* v_c
  *     bf16): an element stands for its e4m3 value times the scale of its page
  *     and head.  masw_paged_append writes powers of two in [2^-64, 2^119];
  *     masw_paged_attn takes any positive finite scale in that range.
- *   page_table: device int [batch][table_stride].  Entries of pages at or behind
- *     a sequence's end are not read.  Sequences may share pages that none of them
+ *   page_table: device int [batch][table_stride].  Entries of pages behind
+ *     a sequence's end are not read, nor, by attention with a window, those of pages
+ *     that lie wholly before the first key that some query sees.  Sequences may share pages that none of them
  *     appends to.
  * head_dim 64 or 128; page_size 16, 32, 64, 128 or 256; batch <= MASW_MAX_BATCH;
  * table_stride * page_size below 2^31.  Page ids outside [0, n_pages) and lengths
@@ -402,15 +403,16 @@ int masw_paged_append(const masw_paged_t* cache, const int* kv_len, const int* r
  * dense; a multiple of 8); n_q_heads a multiple of n_kv_heads, at most 128 query
  * heads per kv head.  max_rows: at least every n_b (NULL row_start: ignored).
  * o: device [rows][n_q_heads][head_dim], bf16 or float (o_dtype), dense, 16-byte
- * aligned; lse: device float [rows][n_q_heads] or NULL.  scale 0 ->
+ * aligned, apart from q; lse: device float [rows][n_q_heads] or NULL.  scale 0 ->
  * 1/sqrt(head_dim).  Keys behind a sequence's end may hold anything, NaN included.
  * A non-finite value at a key that a sequence's queries partly see may reach those
  * of its rows that share a tile with a row that sees it.
  * Scores, softmax statistics and sums are fp32.  With e4m3 pages Q enters the
  * matrix products as two e4m3 terms (exact but for what lies 2^-18 below the
- * largest element of its row, or of the pair's rows when they are few) and so does
- * each weight (off by at most 2^-9 of itself or 2^-16 of the largest); with bf16
- * pages a weight enters as bf16.
+ * largest element of its row, or of the pair's rows when they are few).  With at
+ * most 32 rows a kv head (max_rows * n_q_heads / n_kv_heads) a weight enters as two
+ * terms: e4m3 (off by at most 2^-9 of itself or 2^-16 of the largest), or bf16 with
+ * bf16 pages (2^-17); with more rows as fp16 (2^-11), or bf16 with bf16 pages (2^-8).
  * workspace: device scratch of masw_paged_workspace_bytes() bytes, 16-byte
  * aligned; needs no initialisation and must not be shared by calls that overlap on
  * the GPU.  status: device int or NULL; the call writes there MASW_EINVAL for a
