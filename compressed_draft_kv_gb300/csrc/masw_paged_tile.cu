@@ -73,8 +73,8 @@ struct Cfg {
     // e4m3: the bf16 rows of Q land where V will be widened
     static constexpr uint32_t kOffLand = E4 ? kOffW : kOffQ;
     static constexpr uint32_t kOffMeta = kOffW + kWS * kWideB;
-    static constexpr uint32_t kOffRow = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);   // a float a row
-    static constexpr uint32_t kOffBar = kOffRow + 2 * kTile * 4;
+    static constexpr uint32_t kOffRow = kOffMeta + (E4 ? kMeta * 8 * 16 : 0);   // a float a row of both tiles; the second's references
+    static constexpr uint32_t kOffBar = kOffRow + 3 * kTile * 4;
     static constexpr int kKFull = 0, kKFree = kKS, kVFull = 2 * kKS, kVFree = kVFull + kVS, kWFull = kVFree + kVS, kWFree = kWFull + kWS, kMetaBar = kWFree + kWS;
     static constexpr int kSFull = kMetaBar + (E4 ? kMeta : 0), kGo = kSFull + 2, kOFull = kGo + 2;   // kGo: all that a step of a tile needs
     static constexpr int kQLand = kOFull + 2;
@@ -92,6 +92,8 @@ struct Cfg {
 
 // Barrier of the two warps (64 threads) that hold the same 32 rows, and their vote.
 __device__ __forceinline__ void bar_pair(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+// the four warps of both tiles that hold the same 32 rows
+__device__ __forceinline__ void bar_quad(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool bar_pair_or(int id, bool x) {
     uint32_t r;
     asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
@@ -132,8 +134,12 @@ __device__ __forceinline__ void unit_of(const TilePlan& plan, int unit, int pair
     h = pair - b * Hkv;
 }
 
-// NS: pages that half a tile of keys (64) touches, as far as scales go: 1, 2 or 4
-template <bool E4, int D, int NS>
+// NS: pages that half a tile of keys (64) touches, as far as scales go: 1, 2 or 4.
+// One: no sequence has more rows than one tile.  The second tile then takes the
+// same rows through every other tile of keys, and the two are joined at the end (16 rows of
+// 4 heads at 20K, 3 sequences: 50 us, with the second tile idle 61; as a run-time choice
+// it cost the chunks with two full tiles 2 to 5%).
+template <bool E4, int D, int NS, bool One>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ PagedAttnParams p, const TilePlan plan) {
     using C = Cfg<E4, D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -169,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         return;
     }
     const int first_tile = it.t0 + j0;
-    const bool two = it.tok1 - it.tok0 > tokens;                       // the second tile has rows
+    // the second tile has rows of its own
+    const bool two = !One && it.tok1 - it.tok0 > tokens;
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tslot)) : "memory");
@@ -196,46 +203,54 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 16) {
             // ---------------- matrix products ----------------
-            // one lane does it all: step j of tile x is P V of key tile j - 1 and S of
-            // key tile j
+            // one lane does it all: step k of tile x is P V of its tile of keys k - 1 and S
+            // of its tile of keys k
             if (elect_one()) {
-                uint32_t ks = 0, ws = 0;                 // stage of K(j), buffer of V(j - 1)
-                for (int j = 0; ok && j <= nt; ++j) {
-                    const uint64_t bv = smem_desc(sb + C::kOffW + ws * C::kWideB, C::kWPanel, 1024, 2);
-                    const uint64_t bk = smem_desc(sb + C::kOffK + ks * C::kTileB, 16, C::kAtom, C::kSwz);
-                    for (int x = 0; x < (two ? 2 : 1); ++x) {
-                        if (!wait(C::kGo + x, j)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t aq = E4 ? smem_desc(sb + C::kOffQ + x * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0)
-                                               : smem_desc(sb + C::kOffQ + x * C::kTileB, 16, 1024, 2);
-                        const uint32_t ts = tmem + C::kColS + x * 128, to = tmem + C::kColO + x * 128;
-                        if (j > 0) {
+                uint32_t ks = 0, ws = 0;                 // stage of K, buffer of V
+                auto step = [&](int x, int xq, int k, bool last, uint64_t bv, uint64_t bk) {
+                    if (!wait(C::kGo + x, k)) return false;
+                    tc_fence_after();
+                    const uint64_t aq = E4 ? smem_desc(sb + C::kOffQ + xq * C::kTerms * C::kTileB, 128, (C::kRB / 16) * 128, 0)
+                                           : smem_desc(sb + C::kOffQ + xq * C::kTileB, 16, 1024, 2);
+                    const uint32_t ts = tmem + C::kColS + x * 128, to = tmem + C::kColO + x * 128;
+                    if (k > 0) {
 #pragma unroll
-                            for (int kk = 0; kk < kTile / 16; ++kk)
-                                umma_bf16_ts(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, bv + (uint64_t)((kk * 2048) >> 4), C::kIdescO, j > 1 || kk > 0);
-                            umma_commit(bar_at((E4 ? C::kWFree : C::kVFree) + ws));
-                            if (j == nt) umma_commit(bar_at(C::kOFull + x));
-                        }
-                        if (j < nt) {
-#pragma unroll
-                            for (int t = 0; t < C::kTerms; ++t)
-#pragma unroll
-                                for (int kk = 0; kk < C::kRB / 32; ++kk) {
-                                    const uint32_t panel = (kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32;
-                                    const uint64_t a = aq + (uint64_t)((E4 ? t * C::kTileB + kk * 256 : panel) >> 4);
-                                    const uint64_t bb = bk + (uint64_t)(panel >> 4);
-                                    if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
-                                    else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
-                                }
-                            umma_commit(bar_at(C::kSFull + x));
-                            umma_commit(bar_at(C::kKFree + ks));
-                        }
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            umma_bf16_ts(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, bv + (uint64_t)((kk * 2048) >> 4), C::kIdescO, k > 1 || kk > 0);
+                        umma_commit(bar_at((E4 ? C::kWFree : C::kVFree) + ws));
+                        if (last) umma_commit(bar_at(C::kOFull + x));
                     }
-                    ks = ks + 1 == C::kKS ? 0 : ks + 1;
-                    if (j > 0) ws = ws + 1 == C::kWS ? 0 : ws + 1;
+                    if (!last) {
+#pragma unroll
+                        for (int t = 0; t < C::kTerms; ++t)
+#pragma unroll
+                            for (int kk = 0; kk < C::kRB / 32; ++kk) {
+                                const uint32_t panel = (kk / (C::kPB / 32)) * C::kPanel + (kk % (C::kPB / 32)) * 32;
+                                const uint64_t a = aq + (uint64_t)((E4 ? t * C::kTileB + kk * 256 : panel) >> 4);
+                                const uint64_t bb = bk + (uint64_t)(panel >> 4);
+                                if (E4) umma_f8(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                                else umma_bf16(ts, a, bb, C::kIdescS, t > 0 || kk > 0);
+                            }
+                        umma_commit(bar_at(C::kSFull + x));
+                        umma_commit(bar_at(C::kKFree + ks));
+                    }
+                    return true;
+                };
+                auto v_at = [&]() { return smem_desc(sb + C::kOffW + ws * C::kWideB, C::kWPanel, 1024, 2); };
+                auto k_at = [&]() { return smem_desc(sb + C::kOffK + ks * C::kTileB, 16, C::kAtom, C::kSwz); };
+                if constexpr (One) {                     // key tiles 2 k + x - 2 and 2 k + x
+                    for (int s = 0; ok && s < nt + 2; ++s) {
+                        ok = step(s & 1, 0, s >> 1, s >= nt, v_at(), k_at());
+                        ks = ks + 1 == C::kKS ? 0 : ks + 1;
+                        if (s > 1) ws = ws + 1 == C::kWS ? 0 : ws + 1;
+                    }
+                } else {                                 // key tiles k - 1 and k
+                    for (int k = 0; ok && k <= nt; ++k) {
+                        const uint64_t bv = v_at(), bk = k_at();
+                        for (int x = 0; ok && x < (two ? 2 : 1); ++x) ok = step(x, x, k, k == nt, bv, bk);
+                        ks = ks + 1 == C::kKS ? 0 : ks + 1;
+                        if (k > 0) ws = ws + 1 == C::kWS ? 0 : ws + 1;
+                    }
                 }
             }
             __syncwarp();
@@ -264,11 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             }
             __syncwarp();
             ok = all(wait(C::kQLand, 0));
-            for (int j = 0; ok && j <= nt; ++j) {
-                if (j < nt) ok = all(wait(C::kKFull + j % C::kKS, j / C::kKS));
-                if (j > 0) ok = ok && all(wait(C::kWFull + (j - 1) % C::kWS, (j - 1) / C::kWS));
-                for (int x = 0; ok && x < (two ? 2 : 1); ++x) {
-                    if (j > 0) ok = all(wait(C::kGo + x, j - 1));   // one arrival a phase
+            for (int s = 0; ok && s < nt + (One ? 2 : 1); ++s) {
+                const int vt = s - (One ? 2 : 1);        // key tile of P V; that of S is s
+                if (s < nt) ok = all(wait(C::kKFull + s % C::kKS, s / C::kKS));
+                if (vt >= 0) ok = ok && all(wait(C::kWFull + vt % C::kWS, vt / C::kWS));
+                for (int x = One ? s & 1 : 0; ok && x < (One ? (s & 1) + 1 : two ? 2 : 1); ++x) {
+                    const int k = One ? s >> 1 : s;
+                    if (k > 0) ok = all(wait(C::kGo + x, k - 1));   // one arrival a phase
                     if (ok && lane == 0) mbar_arrive(bar_at(C::kGo + x));
                 }
             }
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         } else {
             // ---------------- V as the products read it: thread t row t of the tile ----------------
             const int t = tid & 127;
-            if (E4) ok = all(wait(C::kGo, 0)) && (!two || all(wait(C::kGo + 1, 0)));   // Q was read from where V goes
+            if (E4) ok = all(wait(C::kGo, 0)) && (!(One || two) || all(wait(C::kGo + 1, 0)));   // Q was read from where V goes
             for (int j = 0; ok && j < nt; ++j) {
                 const int key = (first_tile + j) * kTile + t, st = j % C::kVS;
                 const bool seen = key >= it.lo && key < it.hi;   // by some row; a row that none sees must not reach the product
@@ -417,19 +434,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             if (hf) mine = *slot;
             return mine;
         };
-        const int tok_first = it.tok0 + x * tokens;                       // of the tile
+        const int tok_first = it.tok0 + (One ? 0 : x * tokens);           // of the tile
         const int tok_last = imin(it.tok1, tok_first + tokens) - 1;
         const int tok = imin(tok_first + r / G, tok_last), g = r % G;
-        const bool live = r < (tok_last - tok_first + 1) * G;             // rows behind repeat the last token
         const int pos = s.kv - s.n + tok;
         const size_t row = (size_t)(s.r0 + tok) * p.Hq + (size_t)h * G + g;
-        if (x == 0 || two) {
+        if (One || x == 0 || two) {
             // Q: this row's half, split into its terms
             float qs = 1.f;
             if constexpr (E4) {
                 ok = wait(C::kQLand, 0);
-                const uint32_t src = sb + C::kOffLand + x * (C::kWPanels * C::kWPanel) + (D == 128 ? hf * C::kWPanel : 0) + r * 128;
-                const uint32_t dst = sb + C::kOffQ + x * C::kTerms * C::kTileB + (uint32_t)((r >> 3) * (C::kRB / 16) * 128 + (r & 7) * 16) +
+                const int xq = One ? 0 : x;
+                const uint32_t src = sb + C::kOffLand + xq * (C::kWPanels * C::kWPanel) + (D == 128 ? hf * C::kWPanel : 0) + r * 128;
+                const uint32_t dst = sb + C::kOffQ + xq * C::kTerms * C::kTileB + (uint32_t)((r >> 3) * (C::kRB / 16) * 128 + (r & 7) * 16) +
                                      (uint32_t)(hf * (C::kRB / 32) * 128);
                 auto chunk_of = [&](int k) {   // eight elements
                     const int ch = D == 128 ? k : hf * 4 + k;
@@ -446,8 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 }
                 qs = pow2_scale(both(amax, [](float a, float b) { return fmaxf(a, b); }));
                 const float inv = 1.f / qs;
+                const int chunks = x == xq ? D / 16 : 0;   // the first tile's warps have split the rows of both
 #pragma unroll 2
-                for (int k = 0; k < D / 16; ++k) {
+                for (int k = 0; k < chunks; ++k) {
                     const float4 v = chunk_of(k);
                     float f[8];
                     Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(&v), f);
@@ -476,7 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
             const int all_hi = s.kv - s.n + tok_first + 1;
             const int all_lo = p.window > 0 ? imax(0, s.kv - s.n + tok_last - p.window + 1) : 0;
             float mref = -INFINITY, l = 0.f;   // the row's reference (the same in both threads) and this half's sum
-            for (int j = 0; j < nt; ++j) {
+            constexpr int half = One ? 1 : 0;   // a tile takes every key tile, or every other one
+            for (int j = half * x; j < nt; j += 1 + half) {
                 const int tile0 = (first_tile + j) * kTile;
                 float ks[NS], lvs[NS], ivs[NS];
                 if constexpr (E4) {
@@ -493,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     ks[0] = qk;
                     lvs[0] = 0.f;
                 }
-                ok &= wait(C::kSFull + x, j);
+                ok &= wait(C::kSFull + x, j >> half);
                 __syncwarp();
                 tc_fence_after();
                 constexpr int kCols = kTile / 2;
@@ -562,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         mref = up;
                         l *= alpha;
                     }
-                    if (j > 0) {
-                        // S(j) done means that P V of the tile before it is; this thread
+                    if (j > half) {
+                        // S(k) done means that P V of the tile before it is; this thread
                         // scales its half of the row's O
 #pragma unroll 1
                         for (int q = hf * (D / 2); q < (hf + 1) * (D / 2); q += 16) {
@@ -587,7 +606,27 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 if (lane == 0) mbar_arrive(bar_at(C::kGo + x));
             }
             l = both(l, [](float a, float b) { return a + b; });
-            ok &= wait(C::kOFull + x, 0);
+            float w0 = 1.f, w1 = 0.f;   // of this tile's outputs and, joined, of the second one's
+            const bool join = One && nt > 1;
+            if constexpr (One) {
+                float* second = reinterpret_cast<float*>(smem + C::kOffRow) + kTile + r;
+                if (x == 1 && hf == 0) {
+                    second[0] = l;
+                    second[kTile] = mref;
+                }
+                bar_quad(9 + (warp & 3));
+                if (x == 0) {
+                    const float l1 = second[0], m1 = second[kTile], m = fmaxf(mref, m1);
+                    w0 = mref == -INFINITY ? 0.f : ex2_approx(mref - m);
+                    w1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m);
+                    l = l * w0 + l1 * w1;
+                    mref = m;
+                }
+            }
+            const bool mine = !One || x == 0;   // the outputs are this warp's to store
+            const bool live = mine && r < (tok_last - tok_first + 1) * G;     // rows behind repeat the last token
+            if (mine) ok &= wait(C::kOFull + x, 0);
+            if (mine && join) ok &= wait(C::kOFull + 1, 0);
             __syncwarp();
             tc_fence_after();
             float* part = nullptr;
@@ -601,11 +640,25 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                 p.lse[row] = l == 0.f ? -INFINITY : (mref + __log2f(l)) * 0.6931471805599453f;
             }
             const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+            w0 *= inv;
+            w1 *= inv;
 #pragma unroll 1
-            for (int q = hf * (D / 2); q < (hf + 1) * (D / 2); q += 32) {
+            for (int q = hf * (D / 2); q < (mine ? (hf + 1) * (D / 2) : 0); q += 32) {
                 uint32_t ov[32];
                 tmem_ld32(t_o + q, ov);
                 tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * w0);
+                if (join) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t o1[8];
+                        tmem_ld8(t_o + 128 + q + e, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ov[e + i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), w1, __uint_as_float(ov[e + i])));
+                    }
+                }
                 if (!live) continue;
                 if (part) {
 #pragma unroll
@@ -614,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                     float* dst = reinterpret_cast<float*>(p.o) + row * D + q;
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
-                        __stcg(reinterpret_cast<float2*>(dst + e), make_float2(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv));
+                        __stcg(reinterpret_cast<float2*>(dst + e), make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])));
                 } else {
                     uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + q);
 #pragma unroll
@@ -622,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                         uint32_t w[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            w[k] = pack_bf16(__uint_as_float(ov[8 * e + 2 * k]) * inv, __uint_as_float(ov[8 * e + 2 * k + 1]) * inv);
+                            w[k] = pack_bf16(__uint_as_float(ov[8 * e + 2 * k]), __uint_as_float(ov[8 * e + 2 * k + 1]));
                         dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
@@ -686,7 +739,7 @@ __global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__
     if (d0 == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
 }
 
-template <bool E4, int D, int NS>
+template <bool E4, int D, int NS, bool One>
 cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st) {
     using C = Cfg<E4, D>;
     static std::atomic<bool> configured[64];
@@ -694,11 +747,11 @@ cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!configured[dev & 63].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(tile_kernel<E4, D, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        e = cudaFuncSetAttribute(tile_kernel<E4, D, NS, One>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         configured[dev & 63].store(true, std::memory_order_release);
     }
-    e = masw_launch(tile_kernel<E4, D, NS>, dim3(plan.whole + plan.cut * plan.n_split), dim3(kThreads), C::kSmem, st, 1, p, plan);
+    e = masw_launch(tile_kernel<E4, D, NS, One>, dim3(plan.whole + plan.cut * plan.n_split), dim3(kThreads), C::kSmem, st, 1, p, plan);
     if (e != cudaSuccess || plan.cut == 0) return e;
     return masw_launch(tile_merge_kernel<D>, dim3(plan.cut, D / 32), dim3(256), 0, st, 1, p, plan);
 }
@@ -706,10 +759,18 @@ cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t 
 }  // namespace tile
 
 cudaError_t launch_paged_tiles(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t st) {
-    if (!p.c.k_scale) return p.c.D == 64 ? tile::launch<false, 64, 1>(p, plan, st) : tile::launch<false, 128, 1>(p, plan, st);
-    if (p.c.P >= 64) return p.c.D == 64 ? tile::launch<true, 64, 1>(p, plan, st) : tile::launch<true, 128, 1>(p, plan, st);
-    if (p.c.P == 32) return p.c.D == 64 ? tile::launch<true, 64, 2>(p, plan, st) : tile::launch<true, 128, 2>(p, plan, st);
-    return p.c.D == 64 ? tile::launch<true, 64, 4>(p, plan, st) : tile::launch<true, 128, 4>(p, plan, st);
+    auto pick = [&](auto e4, auto d, auto ns) {
+        constexpr bool E4 = decltype(e4)::value;
+        constexpr int D = decltype(d)::value, NS = decltype(ns)::value;
+        return p.max_rows <= kTile / p.G ? tile::launch<E4, D, NS, true>(p, plan, st) : tile::launch<E4, D, NS, false>(p, plan, st);
+    };
+    auto by_dim = [&](auto e4, auto ns) {
+        return p.c.D == 64 ? pick(e4, std::integral_constant<int, 64>{}, ns) : pick(e4, std::integral_constant<int, 128>{}, ns);
+    };
+    if (!p.c.k_scale) return by_dim(std::false_type{}, std::integral_constant<int, 1>{});
+    if (p.c.P >= 64) return by_dim(std::true_type{}, std::integral_constant<int, 1>{});
+    if (p.c.P == 32) return by_dim(std::true_type{}, std::integral_constant<int, 2>{});
+    return by_dim(std::true_type{}, std::integral_constant<int, 4>{});
 }
 
 }  // namespace masw
