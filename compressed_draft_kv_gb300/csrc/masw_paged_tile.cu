@@ -28,8 +28,8 @@
 // sees.  A long cache under few rows is cut into splits, whose partial results a second
 // kernel joins.
 //
-// Measured: a 2K chunk at 32K, 32 query and 8 kv heads of 128, e4m3: 774 us (1376
-// TFLOP/s); prompts of up to 4K, 24 query heads, bf16: 235 us (870 TFLOP/s: a CTA's start
+// Measured: a 2K chunk at 32K, 32 query and 8 kv heads of 128, e4m3: 765 us (1393
+// TFLOP/s); prompts of up to 4K, 24 query heads, bf16: 240 us (850 TFLOP/s: a CTA's start
 // and end, ~9 us, against a mean of 8 tiles of keys).  A tile of keys for both tiles
 // of rows takes ~2.9K cycles, of which the matrix products are ~2.1K.
 #include "masw_paged_attn.cuh"
@@ -137,7 +137,7 @@ __device__ __forceinline__ void unit_of(const TilePlan& plan, int unit, int pair
 // NS: pages that half a tile of keys (64) touches, as far as scales go: 1, 2 or 4.
 // One: no sequence has more rows than one tile.  The second tile then takes the
 // same rows through every other tile of keys, and the two are joined at the end (16 rows of
-// 4 heads at 20K, 3 sequences: 50 us, with the second tile idle 61; as a run-time choice
+// 4 heads, 32 sequences at 4K: 94 us, with the second tile idle 122; as a run-time choice
 // it cost the chunks with two full tiles 2 to 5%).
 template <bool E4, int D, int NS, bool One>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ PagedAttnParams p, const TilePlan plan) {
@@ -692,14 +692,17 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
 }
 
-// Joins the splits of an item: thread r row r of its 256, 32 elements a CTA.
+// Joins the splits of an item: thread r row r of its 256, 8 elements a CTA, four
+// splits' loads at a time (one sequence, 16 rows at 32K, 19 splits: 32 us; one by one, 32
+// elements a CTA: 53).
+constexpr int kMergeElems = 8, kAtOnce = 4;
 template <int D>
 __global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__ PagedAttnParams p, const TilePlan plan) {
     const PagedView& c = p.c;
     pdl_wait();
     pdl_trigger();
     const int G = p.G, tokens = kTile / G, n_split = plan.n_split, r = threadIdx.x;
-    const int over = blockIdx.x, d0 = (int)blockIdx.y * 32;
+    const int over = blockIdx.x, d0 = (int)blockIdx.y * kMergeElems;
     int b, h, item;
     unit_of(plan, plan.whole + over, c.B * c.Hkv, c.Hkv, b, h, item);
     const SeqRows s = seq_rows(p.row_start, p.kv_len, b, p.rows, c.B, c.cap);
@@ -708,33 +711,50 @@ __global__ void __launch_bounds__(256) tile_merge_kernel(const __grid_constant__
     if (it.nt < plan.min_tiles) return;
     const int tok = it.tok0 + (r >> 7) * tokens + (r & 127) / G;
     if ((r & 127) >= tokens * G || tok >= it.tok1) return;
-    const int chunk = (it.nt + n_split - 1) / n_split;
-    float M = -INFINITY, l = 0.f, o[32] = {};
-    for (int q = 0; q < n_split && q * chunk < it.nt; ++q) {
-        const float* part = p.part + ((size_t)over * n_split + q) * 256 * (D + 2) + r;
-        const float m = __ldcg(part + D * 256), pl = __ldcg(part + (D + 1) * 256);
-        float v[32];
+    const int chunk = (it.nt + n_split - 1) / n_split, pieces = (it.nt + chunk - 1) / chunk;
+    float M = -INFINITY, l = 0.f, o[kMergeElems] = {};
+    for (int q0 = 0; q0 < pieces; q0 += kAtOnce) {
+        float m[kAtOnce], pl[kAtOnce], v[kAtOnce][kMergeElems];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __ldcg(part + (d0 + e) * 256);
-        if (m == -INFINITY) continue;
-        const float nm = fmaxf(M, m), w0 = exp2f(M - nm), w1 = exp2f(m - nm);
-        l = l * w0 + pl * w1;
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int q = imin(q0 + k, pieces - 1);
+            const float* part = p.part + ((size_t)over * n_split + q) * 256 * (D + 2) + r;
+            m[k] = __ldcg(part + D * 256);
+            pl[k] = __ldcg(part + (D + 1) * 256);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + v[e] * w1;
-        M = nm;
+            for (int e = 0; e < kMergeElems; ++e) v[k][e] = __ldcg(part + (d0 + e) * 256);
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (q0 + k >= pieces) m[k] = -INFINITY;
+            top = fmaxf(top, m[k]);
+        }
+        if (top == -INFINITY) continue;
+        const float w = exp2f(M - top);
+        l *= w;
+#pragma unroll
+        for (int e = 0; e < kMergeElems; ++e) o[e] *= w;
+        M = top;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (m[k] == -INFINITY) continue;   // its outputs are not used, whatever they are
+            const float wk = exp2f(m[k] - M);
+            l = fmaf(pl[k], wk, l);
+#pragma unroll
+            for (int e = 0; e < kMergeElems; ++e) o[e] = fmaf(v[k][e], wk, o[e]);
+        }
     }
     const size_t row = (size_t)(s.r0 + tok) * p.Hq + (size_t)h * G + (r & 127) % G;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (p.o_f32) {
         float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + row * D + d0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+        dst[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        dst[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
     } else {
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + d0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o) + row * D + d0) =
+            make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv), pack_bf16(o[4] * inv, o[5] * inv),
+                       pack_bf16(o[6] * inv, o[7] * inv));
     }
     if (d0 == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
 }
@@ -753,7 +773,7 @@ cudaError_t launch(const PagedAttnParams& p, const TilePlan& plan, cudaStream_t 
     }
     e = masw_launch(tile_kernel<E4, D, NS, One>, dim3(plan.whole + plan.cut * plan.n_split), dim3(kThreads), C::kSmem, st, 1, p, plan);
     if (e != cudaSuccess || plan.cut == 0) return e;
-    return masw_launch(tile_merge_kernel<D>, dim3(plan.cut, D / 32), dim3(256), 0, st, 1, p, plan);
+    return masw_launch(tile_merge_kernel<D>, dim3(plan.cut, D / kMergeElems), dim3(256), 0, st, 1, p, plan);
 }
 
 }  // namespace tile
