@@ -385,7 +385,7 @@ typedef struct {
  * not depend on timing.  A scale never shrinks while its page is being filled:
  * after drafts were rejected (a shorter kv_len), the next append overwrites their
  * rows and keeps the scale.
- * No page may be appended to for two sequences in one call.  status: device int
+ * No page may be appended to from two table entries in one call.  status: device int
  * or NULL; the call writes MASW_EINVAL there when it met a bad length, row range,
  * page id or position (and skips what it cannot place), and nothing otherwise. */
 int masw_paged_append(const masw_paged_t* cache, const int* kv_len, const int* row_start, int rows,
