@@ -158,11 +158,18 @@ __device__ __forceinline__ void rescale16(uint8_t* at, float f) {
     *reinterpret_cast<uint4*>(at) = w;
 }
 // x / sc as e4m3.  A power of two (every scale this file makes; a pool filled
-// elsewhere may hold others) divides exactly by a multiplication.
-__device__ __forceinline__ void store_e4m3(uint8_t* dst, const LaneChunks& lc, const float (&x)[16], float sc) {
+// elsewhere may hold others) divides exactly by a multiplication, and where no
+// infinity is among the values (`inf`) the conversion needs no check (NaN stays NaN).
+__device__ __forceinline__ void store_e4m3(uint8_t* dst, const LaneChunks& lc, const float (&x)[16], float sc, bool inf) {
     const uint32_t bits = __float_as_uint(sc);
     uint32_t w[4];
-    if ((bits & 0x807fffffu) == 0u && bits >= 0x00800000u && bits <= 0x7e000000u) {
+    const bool pow2 = (bits & 0x807fffffu) == 0u && bits >= 0x00800000u && bits <= 0x7e000000u;
+    if (pow2 && !inf) {
+        const float f = __uint_as_float(0x7f000000u - bits);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = e4m3x2_no_inf(x[4 * i] * f, x[4 * i + 1] * f) | (e4m3x2_no_inf(x[4 * i + 2] * f, x[4 * i + 3] * f) << 16);
+    } else if (pow2) {
         const float f = __uint_as_float(0x7f000000u - bits);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -241,7 +248,7 @@ __global__ void __launch_bounds__(256, 3) paged_append_step_kernel(const __grid_
         for (int r = sub; r < w.off; r += R) rescale16(base + (size_t)r * c.D + 16 * t, old / sc);
     for (int pos = first; pos < w.rb; pos += R) {
         if (pos > first) load(pos, x0);
-        store_e4m3(base + (size_t)(pos % P) * c.D, lc, x0, sc);
+        store_e4m3(base + (size_t)(pos % P) * c.D, lc, x0, sc, true);
     }
     if (t == 0 && sub == 0) *sp = sc;
 }
@@ -249,11 +256,13 @@ __global__ void __launch_bounds__(256, 3) paged_append_step_kernel(const __grid_
 // Many rows a unit.  A CTA of P D / (16 NP) threads holds a whole (page, head) in
 // fp32 registers, NP rows a thread: one read, the largest magnitude over the
 // CTA, one write.  It does `hg` heads one after the other, the next ones' rows on their
-// way to shared memory (kStages: 2 119 us, 3 112, 4 113), and keeps the cosines and
-// sines of its rows for all of them; reading them again for every head costs
-// 186 us.  P D = 32768 leaves no registers for that (NP = 4).  Bound by HBM: a 32K
-// prompt of 24 + 2 * 8 heads of 128 into e4m3 pages of 64 tokens takes 112 us,
-// 5.5 TB/s; walking the rows with the other kernel's loop took 268.
+// way to shared memory, and keeps the cosines and sines of its rows for all of them.
+// P D = 32768 leaves no registers for that (NP = 4).  Bound by HBM: a 32K prompt of
+// 24 + 2 * 8 heads of 128 into e4m3 pages of 64 tokens takes 107 us, 5.8 TB/s (112 with
+// every element checked for infinities twice, then 119 with kStages = 2 and 113 with 4,
+// 186 with the angles read again for every head, 124 with the rows rotated again from
+// shared memory instead of held and three CTAs an SM); walking the rows with the other
+// kernel's loop took 268.
 template <int NP>
 __global__ void __launch_bounds__(512) paged_append_page_kernel(const __grid_constant__ PagedAppendParams p, int hg) {
     __shared__ uint32_t s_max[2][16];
@@ -370,11 +379,19 @@ __global__ void __launch_bounds__(512) paged_append_page_kernel(const __grid_con
         float* sp = (is_v ? c.v_scale : c.k_scale) + (size_t)w.pid * c.Hkv + h;
         uint8_t* base = (is_v ? c.v : c.k) + (size_t)w.pid * c.page_bytes + (size_t)h * P * D;
         const float old = w.off > 0 ? *sp : 0.f;   // read by all before the barrier, written behind it
-        float amax = 0.f;
+        float amax = 0.f;   // a maximum passes over NaN, and an infinity shows in it
 #pragma unroll
         for (int j = 0; j < NP; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x[j][i]));
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[j][i]));
+        const bool inf = amax > 3.4028234663852886e38f;
+        if (inf) {
+            amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x[j][i]));
+        }
         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
         if (tid % 32 == 0) s_max[par][tid / 32] = top;
         __syncthreads();
@@ -386,7 +403,7 @@ __global__ void __launch_bounds__(512) paged_append_page_kernel(const __grid_con
             for (int r = tid / L; r < w.off; r += G) rescale16(base + (size_t)r * D + 16 * t, old / sc);
 #pragma unroll
         for (int j = 0; j < NP; ++j)
-            if (has[j]) store_e4m3(base + (size_t)(w.off + j * G + tid / L) * D, lc, x[j], sc);
+            if (has[j]) store_e4m3(base + (size_t)(w.off + j * G + tid / L) * D, lc, x[j], sc, inf);
         if (tid == 0) *sp = sc;
     }
 }

@@ -106,12 +106,15 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 // two fp32 values -> e4m3 (round to nearest even, lo in bits 0..7); what is not
 // finite becomes NaN (the conversion itself would saturate an infinity)
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    lo = fabsf(lo) <= 3.4028234663852886e38f ? lo : __int_as_float(0x7fffffff);
-    hi = fabsf(hi) <= 3.4028234663852886e38f ? hi : __int_as_float(0x7fffffff);
+__device__ __forceinline__ uint32_t e4m3x2_no_inf(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    lo = fabsf(lo) <= 3.4028234663852886e38f ? lo : __int_as_float(0x7fffffff);
+    hi = fabsf(hi) <= 3.4028234663852886e38f ? hi : __int_as_float(0x7fffffff);
+    return e4m3x2_no_inf(lo, hi);
 }
 // two e4m3 values (bits 0..7 and 8..15) -> f16x2
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
